@@ -8,7 +8,9 @@ fallback: if the library is missing, every call raises.
 
 Names follow the C ABI: ``prepack_weights``, ``route``, ``permute``,
 ``grouped_gemm_swiglu``, ``grouped_gemm1_swiglu``, ``grouped_gemm1_preact``,
-``grouped_gemm2``, ``combine``, ``forward``.
+``grouped_gemm2``, ``combine``, ``forward``.  The block around the layer (norms, gate,
+residual) and the layer for few tokens are in ``block.py`` and reached here too:
+``block_norm``, ``block_residual``, ``combine_residual``, ``forward_few``, ``block_forward``.
 """
 
 import ctypes
@@ -355,3 +357,10 @@ def forward_noalloc(p, x, w_router, sel_bias, weights, y, out_dtype=OUT_F32, str
     st = load().moe_forward_noalloc(ctypes.byref(p), _ptr(x), _ptr(w_router), _ptr(sel_bias), ctypes.byref(w),
                                     _ptr(y), int(out_dtype), _stream(stream))
     _raise("moe_forward_noalloc", st)
+
+
+# the decoder block around the layer and the layer for few tokens (include/moe_block.h)
+from .block import *  # noqa: E402,F401,F403
+from .block import __all__ as _block_all  # noqa: E402
+
+__all__ += _block_all

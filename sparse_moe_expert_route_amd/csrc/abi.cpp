@@ -7,6 +7,7 @@
 
 #include <cmath>
 
+#include "abi_checks.h"
 #include "moe.h"
 #include "moe_launch.h"
 
@@ -14,34 +15,15 @@ namespace {
 
 using namespace moe;
 
-constexpr size_t kAlign = 256;
-
 static_assert(kErrExpertIdRange == MOE_DEVERR_EXPERT_ID_RANGE && kErrExpertIdDuplicate == MOE_DEVERR_EXPERT_ID_DUPLICATE &&
                   kErrExpertOffsets == MOE_DEVERR_EXPERT_OFFSETS,
               "device error bits of the kernels and of moe.h");
-
-size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 struct Layout {
     size_t errors, logits, ids, w, offsets, sorted_token, row_of_slot, block_counts, block_base, block_err;
     size_t tile_start, tile_info;
     size_t xq, xs, hq, hs, y_perm, total;
 };
-
-moe_status check_problem(const moe_problem* p) {
-    if (!p) return MOE_ERR_INVALID_ARGUMENT;
-    if (p->num_tokens < 0) return MOE_ERR_INVALID_ARGUMENT;
-    if (p->hidden <= 0 || p->hidden % kFp8Block) return MOE_ERR_INVALID_ARGUMENT;
-    if (p->intermediate <= 0 || p->intermediate % kFp8Block) return MOE_ERR_INVALID_ARGUMENT;
-    if (p->num_experts < 1 || p->num_experts > 512) return MOE_ERR_INVALID_ARGUMENT;
-    if (p->top_k < 1 || p->top_k > 8 || p->top_k > p->num_experts) return MOE_ERR_INVALID_ARGUMENT;
-    if (p->score_func != MOE_SCORE_SOFTMAX_TOPK && p->score_func != MOE_SCORE_SIGMOID_BIAS) return MOE_ERR_UNSUPPORTED;
-    if (p->expert_format != MOE_EXPERTS_MXFP4 && p->expert_format != MOE_EXPERTS_FP8_BLOCK) return MOE_ERR_UNSUPPORTED;
-    if (p->num_tokens * (int64_t)p->top_k >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
-    return MOE_OK;
-}
 
 bool fp8_block(const moe_problem& p) { return p.expert_format == MOE_EXPERTS_FP8_BLOCK; }
 // bytes of one activation / h scale: e8m0, or float32 with FP8 block-scaled experts
@@ -76,42 +58,12 @@ Layout layout_of(const moe_problem& p) {
     return L;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) { return (T*)((char*)ws + off); }
-
 moe_status check_ws(const moe_problem& p, const void* ws, size_t ws_bytes) {
     if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARGUMENT;
     if (((uintptr_t)ws % kAlign) != 0) return MOE_ERR_INVALID_ARGUMENT;
     if (ws_bytes < layout_of(p).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     return MOE_OK;
 }
-
-moe_status check_weights(const moe_expert_weights* w) {
-    if (!w || !w->w13 || !w->w13_scale || !w->w2 || !w->w2_scale) return MOE_ERR_INVALID_ARGUMENT;
-    if (!aligned16(w->w13) || !aligned16(w->w13_scale) || !aligned16(w->w2) || !aligned16(w->w2_scale))
-        return MOE_ERR_INVALID_ARGUMENT;
-    if (w->layout != MOE_WEIGHTS_CANONICAL && w->layout != MOE_WEIGHTS_PACKED) return MOE_ERR_INVALID_ARGUMENT;
-    return MOE_OK;
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
-}
-
-#define MOE_CHECK(expr)                          \
-    do {                                         \
-        const moe_status st_ = (expr);           \
-        if (st_ != MOE_OK) return st_;           \
-    } while (0)
-#define MOE_LAUNCH(expr)                         \
-    do {                                         \
-        if ((expr) != hipSuccess) return MOE_ERR_HIP; \
-    } while (0)
-
-bool all_aligned() { return true; }
-template <typename P, typename... R>
-bool all_aligned(P p, R... rest) { return p && aligned16(p) && all_aligned(rest...); }
 
 // ---- launch sequences (arguments already validated) ----------------------
 

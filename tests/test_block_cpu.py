@@ -1,0 +1,173 @@
+"""The entry points of include/moe_block.h on the CPU: they are exported, and every refusal
+comes back as a status before any HIP call (there is no GPU here)."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import sparse_moe_expert_route_amd as moe
+from sparse_moe_expert_route_amd import block
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, INVALID, UNSUPPORTED, SMALL = 0, 1, 2, 3
+M = 1 << 24   # spacing of the fake addresses; never dereferenced
+BIG = 1 << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.lib_path):
+        from sparse_moe_expert_route_amd import build
+        build.build()
+    return block._load()
+
+
+def _P(T=8, H=256, I=128, E=8, k=2, sf=0, fmt=0):
+    return moe.Problem.make(T, H, I, E, k, sf, fmt)
+
+
+def _tail(**over):
+    f = dict(r=10 * M, r_out=11 * M, w_post=12 * M, gate=13 * M, w_next=14 * M, n_next=15 * M, scale=1.0, eps=1e-6,
+             res_dtype=1, param_dtype=1, post_norm=1, gate_per_token=0)
+    f.update(over)
+    return block._Tail(*f.values())
+
+
+def _w(ptr=20 * M, layout=0):
+    return moe._Weights(ptr, ptr, ptr, ptr, layout)
+
+
+def test_header_declares_the_binding_symbols(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "moe_block.h")).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
+    assert names == sorted(moe.EXPORTED_BLOCK_SYMBOLS)
+    for n in names:
+        assert hasattr(lib, n), n
+    assert "MOE_FEW_MAX_TOKENS %d" % moe.FEW_MAX_TOKENS in text
+    assert "MOE_BLOCK_MAX_HIDDEN %d" % moe.BLOCK_MAX_HIDDEN in text
+
+
+@pytest.mark.parametrize("T,H,I,E,k,fmt", [(1, 4096, 2048, 256, 8, 0), (16, 6144, 2048, 384, 8, 1), (0, 256, 128, 8, 2, 0),
+                                           (8192, 4096, 2048, 256, 8, 0), (16, 128, 128, 1, 1, 0)])
+def test_workspace_size_covers_the_layer_and_the_block(lib, T, H, I, E, k, fmt):
+    p = _P(T, H, I, E, k, 0, fmt)
+    n = moe.block_workspace_size(p)
+    assert n % 256 == 0 and n >= moe.workspace_size(p) + T * H * 6
+    bad = _P(H=100)
+    assert lib.moe_block_workspace_size(ctypes.byref(bad)) == 0
+    assert lib.moe_block_workspace_size(None) == 0
+
+
+def test_norm_refusals(lib):
+    def norm(p=None, r=M, rd=1, w=2 * M, pd=1, eps=1e-6, n=3 * M):
+        return lib.moe_block_norm(_P() if p is None else p, r, rd, w, pd, eps, n, None)
+    assert norm(p=_P(H=100)) == INVALID
+    assert norm(p=_P(H=16384 + 128)) == UNSUPPORTED
+    assert norm(r=None) == INVALID and norm(n=None) == INVALID
+    assert norm(r=M + 8) == INVALID and norm(n=M + 8) == INVALID and norm(w=2 * M + 4) == INVALID
+    assert norm(rd=2) == INVALID and norm(pd=-1) == INVALID
+    for eps in (0.0, -1e-6, float("nan"), float("inf")):
+        assert norm(eps=eps) == INVALID
+    assert norm(n=M) == INVALID                      # n over r
+    assert norm(n=M + 16) == INVALID
+    assert norm(n=2 * M) == INVALID                  # n over w
+    assert norm(p=_P(T=0)) == OK
+    assert norm(p=_P(T=0), w=None) == OK
+
+
+@pytest.mark.parametrize("call", ["residual", "combine", "block"])
+def test_tail_refusals(lib, call):
+    def run(p=None, **over):
+        p = _P() if p is None else p
+        t = _tail(**over)
+        if call == "residual":
+            return lib.moe_block_residual(p, 2 * M, 1, t, None)
+        if call == "combine":
+            return lib.moe_combine_residual(p, 2 * M, 3 * M, 4 * M, t, None)
+        return lib.moe_block_forward(p, 5 * M, 6 * M, None, _w(), t, 64 * M, 1 << 22, None)
+    for name in ("r", "r_out"):
+        assert run(**{name: None}) == INVALID, name
+    for name in ("r", "r_out", "w_post", "gate", "w_next", "n_next"):
+        assert run(**{name: 17 * M + 8}) == INVALID, name
+    assert run(res_dtype=2) == INVALID and run(param_dtype=2) == INVALID
+    assert run(post_norm=2) == INVALID and run(gate_per_token=2) == INVALID
+    for bad in (float("nan"), float("inf")):
+        assert run(scale=bad) == INVALID and run(eps=bad) == INVALID
+    assert run(eps=0.0) == INVALID
+    # outputs over inputs or each other; r_out may be r itself, not a shifted view of it
+    assert run(r_out=10 * M + 512) == INVALID
+    for name in ("w_post", "gate", "w_next"):
+        assert run(**{name: 11 * M}) == INVALID, name
+        assert run(**{name: 15 * M}) == INVALID, name
+    assert run(n_next=10 * M) == INVALID and run(n_next=11 * M + 1024) == INVALID
+    # a gate per token is T rows long
+    assert run(gate=15 * M - 1024, gate_per_token=1) == INVALID          # 4096 bytes: reaches n_next
+    assert run(p=_P(H=16384 + 128)) == UNSUPPORTED
+    assert run(p=_P(T=0)) == OK
+    assert run(p=_P(T=0), r_out=10 * M) == OK
+
+
+def test_residual_and_combine_inputs(lib):
+    p, t = _P(), _tail()
+    assert lib.moe_block_residual(p, None, 1, t, None) == INVALID
+    assert lib.moe_block_residual(p, 2 * M, 5, t, None) == INVALID
+    assert lib.moe_block_residual(p, 11 * M, 1, t, None) == INVALID      # r_out over y
+    assert lib.moe_block_residual(p, 2 * M, 1, None, None) == INVALID
+    assert lib.moe_combine_residual(p, None, 3 * M, 4 * M, t, None) == INVALID
+    assert lib.moe_combine_residual(p, 2 * M, 3 * M + 4, 4 * M, t, None) == INVALID
+    assert lib.moe_combine_residual(p, 15 * M, 3 * M, 4 * M, t, None) == INVALID   # n_next over y_perm
+    assert lib.moe_combine_residual(p, 2 * M, 11 * M, 4 * M, t, None) == INVALID
+
+
+def test_few_refusals(lib):
+    def few(p=None, x=M, wr=2 * M, b=None, w=None, y=3 * M, od=0, ws=64 * M, n=BIG):
+        return lib.moe_forward_few(_P() if p is None else p, x, wr, b, _w() if w is None else w, y, od, ws, n, None)
+    assert few(p=_P(T=17)) == UNSUPPORTED
+    assert few(p=_P(H=200)) == INVALID and few(p=_P(sf=3)) == UNSUPPORTED
+    assert few(x=None) == INVALID and few(wr=None) == INVALID and few(y=None) == INVALID
+    assert few(x=M + 8) == INVALID and few(b=M + 4) == INVALID and few(y=M + 8) == INVALID
+    assert few(od=2) == INVALID and few(w=_w(0)) == INVALID and few(w=_w(layout=3)) == INVALID
+    assert few(ws=None) == INVALID and few(ws=64 * M + 16) == INVALID
+    assert few(n=moe.block_workspace_size(_P()) - 1) == SMALL
+    assert few(p=_P(T=0)) == OK
+
+
+def test_block_forward_refusals(lib):
+    def run(p=None, w_pre=5 * M, wr=6 * M, b=None, w=None, t=None, ws=64 * M, n=BIG):
+        return lib.moe_block_forward(_P() if p is None else p, w_pre, wr, b, _w() if w is None else w,
+                                     _tail() if t is None else t, ws, n, None)
+    assert run(wr=None) == INVALID and run(w_pre=5 * M + 4) == INVALID and run(b=5 * M + 4) == INVALID
+    assert run(w=_w(0)) == INVALID and run(ws=None) == INVALID
+    assert run(n=moe.block_workspace_size(_P()) - 1) == SMALL
+    assert run(w_pre=11 * M) == INVALID and run(wr=15 * M) == INVALID   # outputs over inputs
+    assert run(t=_tail(r_out=64 * M)) == INVALID                        # r_out over the workspace
+    assert run(p=_P(T=0), w_pre=None) == OK
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    p = _P()
+    r = torch.zeros(8, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        moe.block_norm(p, r, None, torch.zeros_like(r))
+    with pytest.raises(ValueError):
+        moe.block_residual(p, r, moe.BlockTail(r, r))
+    # the tail's own checks (device -1: host tensors, so the shapes and types are what is tested)
+    def bad(**over):
+        a = dict(r=r, r_out=r, w_post=torch.ones(256), gate=None, w_next=None, n_next=None)
+        a.update(over)
+        with pytest.raises(ValueError):
+            moe.BlockTail(a.pop("r"), a.pop("r_out"), **a).struct(p, -1)
+    bad(r=r.half())
+    bad(r_out=r.float())
+    bad(r_out=r[:4])
+    bad(w_post=torch.ones(128))
+    bad(gate=torch.ones(256, dtype=torch.bfloat16))             # another type than w_post
+    bad(gate=torch.ones(7, 256))
+    bad(gate=torch.ones(256, 8).t())                            # strided
+    bad(w_post=torch.ones(256, dtype=torch.float16))
+    bad(n_next=torch.zeros(8, 256))
+    s = moe.BlockTail(r, r, gate=torch.ones(8, 256)).struct(p, -1)
+    assert s.gate_per_token == 1 and s.res_dtype == 1 and s.param_dtype == 0 and s.post_norm == 1

@@ -1,0 +1,249 @@
+"""GPU parity of the layer for few tokens (moe_forward_few) and of the whole block (moe_block_forward)
+against the float64 oracle.
+
+Tolerances are those of the layer's other parity tests (moe_testutil): 2e-2 RMS plus, on elements the
+oracle flags as ambiguous, one step of an FP8 code of h carried through |W2|.  Tokens whose selection
+lies within the float32 uncertainty of their logits of a tie are compared by nothing but finiteness.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import synthetic as S
+from moe_testutil import (dev, host, log, weights, problem, unambiguous_tokens, key_margin, oracle_with_allowance,
+                          check_output, bf16_rne, LOGIT_RTOL)
+from oracle import block as OB
+from oracle import layer as OL
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import sparse_moe_expert_route_amd as m
+    m.load()
+    return m
+
+
+def make(over):
+    over = dict(over)
+    score = over.pop("score", "softmax")
+    same = over.pop("same", False)
+    lay = S.make_layer("tiny", seed=over.pop("seed", 0), **over)
+    lay["score"] = score
+    if same:       # every token to the same experts: a bias far above any score
+        E, k = lay["w13"].shape[0], lay["top_k"]
+        b = np.zeros(E, np.float32)
+        b[np.random.default_rng(3).permutation(E)[:k]] = 100.0
+        lay["bias"] = b
+    return lay
+
+
+def guarded(T, H, dtype):
+    buf = torch.full((T + 2, H), 77.0, dtype=dtype, device="cuda")
+
+    def check():
+        assert torch.all(buf[0] == 77.0) and torch.all(buf[T + 1] == 77.0)
+    return buf[1:T + 1], check
+
+
+def clear_tokens(lay, L_ref):
+    """Tokens whose selected set is beyond the float32 error of the logits (a generous 1e-5 RMS)."""
+    L = L_ref + 1e-5 * np.sqrt(np.mean(L_ref ** 2))
+    return unambiguous_tokens(L_ref, lay["top_k"], lay["bias"], key_margin(L, L_ref, lay["bias"], lay["score"]),
+                              order=False, score=lay["score"])
+
+
+CASES = [dict(T=1), dict(T=16), dict(T=7, E=32, k=4, bias="zipf"), dict(T=1, H=128, I=128, E=1, k=1),
+         dict(T=16, H=128, I=128, E=1, k=1), dict(T=2, E=4, k=4), dict(T=16, E=512, k=8, H=512, I=256),
+         dict(T=3, E=130, k=8), dict(T=13, E=65, k=5, H=384, I=384), dict(T=5, H=1024, I=640, E=12, k=3),
+         dict(T=16, H=640, I=1152, E=24, k=8), dict(T=4, H=2176, I=128, E=16, k=2), dict(T=9, H=256, I=2048, E=8, k=6),
+         dict(T=16, E=64, k=8, H=512, I=512, same=True), dict(T=15, E=16, k=3, same=True),
+         dict(T=8, H=4096, I=2048, E=16, k=8), dict(T=2, H=6144, I=512, E=16, k=8), dict(T=1, H=8192, I=256, E=8, k=4),
+         dict(T=2, H=16512, I=128, E=4, k=2)]
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8_block"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_forward_few_parity(moe, case, fmt, packed):
+    over = dict(CASES[case], format=fmt, score="sigmoid" if case % 3 == 2 else "softmax")
+    log("forward_few %s packed=%s" % (over, packed))
+    lay = make(over)
+    p = problem(lay)
+    W = weights(lay, packed)
+    T, H = lay["x"].shape
+    ws = moe.alloc_block_workspace(p)
+    ws.fill_(0xFF)                               # nothing of the workspace has to start at zero
+    bias = None if lay["bias"] is None else dev(lay["bias"])
+    y, check = guarded(T, H, torch.float32)
+    moe.forward_few(p, dev(lay["x"]), dev(lay["w_router"]), bias, W, y, ws)
+    torch.cuda.synchronize()
+    check()
+    ref = oracle_with_allowance(lay)
+    err, share = check_output(host(y), ref, rows=clear_tokens(lay, ref["logits"]))
+    log("  max err / RMS %.2e, share past the plain bar %.2e" % (err, share))
+    assert np.all(np.isfinite(host(y)))
+    # bf16 output: the rounding of the same float32 sums, from a second call on the same workspace
+    yb, check = guarded(T, H, torch.bfloat16)
+    moe.forward_few(p, dev(lay["x"]), dev(lay["w_router"]), bias, W, yb, ws, moe.OUT_BF16)
+    torch.cuda.synchronize()
+    check()
+    assert np.array_equal(host(yb.contiguous()), bf16_rne(host(y)))
+
+
+def test_rows_do_not_depend_on_their_neighbours(moe):
+    """A token's output has the same bits alone and among others (every step is row-local)."""
+    lay = make(dict(T=16, E=32, k=4, H=1024, I=512))
+    p = problem(lay)
+    W = weights(lay, True)
+    x, wr = dev(lay["x"]), dev(lay["w_router"])
+    y = torch.empty(16, 1024, device="cuda")
+    moe.forward_few(p, x, wr, None, W, y, moe.alloc_block_workspace(p))
+    for t in (0, 7, 15):
+        p1 = moe.Problem.make(1, 1024, 512, 32, 4)
+        y1 = torch.empty(1, 1024, device="cuda")
+        moe.forward_few(p1, x[t:t + 1], wr, None, W, y1, moe.alloc_block_workspace(p1))
+        torch.cuda.synchronize()
+        assert torch.equal(y1[0], y[t]), t
+
+
+def test_selection_ties_go_to_the_lowest_id(moe):
+    """Equal router rows give equal logits: the lowest ids win, as moe_route selects."""
+    E, k, T, H = 48, 6, 4, 256
+    lay = make(dict(T=T, E=E, k=k, H=H, I=128))
+    lay["w_router"] = np.repeat(lay["w_router"][:1], E, axis=0)
+    p = problem(lay)
+    y = torch.empty(T, H, device="cuda")
+    moe.forward_few(p, dev(lay["x"]), dev(lay["w_router"]), None, weights(lay, True), y, moe.alloc_block_workspace(p))
+    torch.cuda.synchronize()
+    ref = oracle_with_allowance(lay)
+    assert np.array_equal(ref["ids"], np.tile(np.arange(k), (T, 1)))
+    check_output(host(y), ref)
+
+
+def test_zero_rows_and_repeats(moe):
+    """An all-zero token gives zeros; repeated calls give the same bits."""
+    lay = make(dict(T=6, E=16, k=4, H=512, I=256))
+    lay["x"][2] = 0
+    p = problem(lay)
+    W, x, wr, ws = weights(lay, True), dev(lay["x"]), dev(lay["w_router"]), moe.alloc_block_workspace(p)
+    y = torch.empty(6, 512, device="cuda")
+    moe.forward_few(p, x, wr, None, W, y, ws)
+    first = y.clone()
+    assert torch.all(y[2] == 0)
+    for _ in range(5):
+        moe.forward_few(p, x, wr, None, W, y, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(first, y)
+
+
+def test_two_streams_and_graph_replays(moe):
+    """Calls that overlap on two streams (a workspace each), and replays of a captured call between eager work."""
+    lays = [make(dict(T=16, E=64, k=8, H=1024, I=512, seed=1)), make(dict(T=5, E=32, k=4, H=2048, I=256, seed=2))]
+    ps = [problem(l) for l in lays]
+    Ws = [weights(l, True) for l in lays]
+    xs, wrs = [dev(l["x"]) for l in lays], [dev(l["w_router"]) for l in lays]
+    wss = [moe.alloc_block_workspace(p) for p in ps]
+    ys = [torch.empty(*x.shape, device="cuda") for x in xs]
+    for i in range(2):
+        moe.forward_few(ps[i], xs[i], wrs[i], None, Ws[i], ys[i], wss[i])
+    torch.cuda.synchronize()
+    want = [y.clone() for y in ys]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for y in ys:
+        y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            moe.forward_few(ps[i], xs[i], wrs[i], None, Ws[i], ys[i], wss[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], want[0]) and torch.equal(ys[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.forward_few(ps[0], xs[0], wrs[0], None, Ws[0], ys[0], wss[0])
+    for i in range(4):
+        ys[0].fill_(float(i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ys[0], want[0])
+        moe.forward_few(ps[1], xs[1], wrs[1], None, Ws[1], ys[1], wss[1])   # eager work between the replays
+        torch.cuda.synchronize()
+        assert torch.equal(ys[1], want[1])
+
+
+BLOCKS = [dict(T=1, E=32, k=4, H=512, I=256), dict(T=16, E=24, k=8, H=1024, I=512, score="sigmoid", bias="zipf"),
+          dict(T=3, E=8, k=2, H=128, I=128, format="fp8_block"), dict(T=40, E=16, k=4, H=512, I=512),
+          dict(T=300, E=8, k=4, H=512, I=512), dict(T=12, E=40, k=6, H=640, I=384, format="fp8_block"),
+          dict(T=2, E=16, k=8, H=6144, I=512), dict(T=5, E=4, k=1, H=2176, I=128)]
+
+
+@pytest.mark.parametrize("case", range(len(BLOCKS)))
+@pytest.mark.parametrize("res,post,gate,in_place", [("f32", True, "row", False), ("bf16", False, None, True),
+                                                    ("bf16", True, "all", False)])
+def test_block_forward_parity(moe, case, res, post, gate, in_place):
+    """The run of the operators together.  The layer's input is held to the oracle's rounding (an element
+    one bf16 step off where float32 meets a border), the output to the layer's bar carried through the tail."""
+    over = BLOCKS[case]
+    log("block_forward %s %s post=%s gate=%s in_place=%s" % (over, res, post, gate, in_place))
+    lay = make(over)
+    p = problem(lay)
+    T, H = lay["x"].shape
+    g = torch.Generator().manual_seed(case)
+    dt = torch.bfloat16 if res == "bf16" else torch.float32
+    par = torch.float32 if case % 2 else torch.bfloat16
+    r = torch.randn(T, H, generator=g).to(dt).cuda()
+    r_in = r.double().cpu().numpy()
+    rnd = lambda *s: (1 + 0.2 * torch.randn(*s, generator=g)).to(par).cuda()
+    w_pre, w_post, w_next = rnd(H), rnd(H) if post else None, rnd(H)
+    gt = None if gate is None else rnd(H) if gate == "row" else rnd(T, H)
+    n_next = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    r_out, check = (r, lambda: None) if in_place else guarded(T, H, dt)
+    tail = moe.BlockTail(r, r_out, post_norm=post, w_post=w_post, gate=gt, scale=0.5, w_next=w_next, n_next=n_next)
+    bias = None if lay["bias"] is None else dev(lay["bias"])
+    ws = moe.alloc_block_workspace(p)
+    ws.fill_(0xFF)
+    W = weights(lay, case % 2 == 0)
+    # the layer's input as the kernel rounds it, from the same norm alone
+    n = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    moe.block_norm(p, r, w_pre, n)
+    torch.cuda.synchronize()
+    moe.block_forward(p, w_pre, dev(lay["w_router"]), bias, W, tail, ws)
+    torch.cuda.synchronize()
+    check()
+    f64 = lambda t: None if t is None else t.double().cpu().numpy()
+    n_ref = OB.rms_norm(r_in, f64(w_pre))
+    assert np.all(np.abs(f64(n) - n_ref) <= np.abs(n_ref) * (2.0 ** -8 + 1e-5))
+    lay["x"] = host(n)
+    ref = oracle_with_allowance(lay)
+    clear = clear_tokens(lay, ref["logits"])
+    y = ref["y"]
+    rms = np.sqrt(np.mean(y ** 2))
+    dy = 2e-2 * rms + ref["allow"]                                  # the layer's bar, per element
+    gg = 1.0 if gt is None else f64(gt)
+    want = OB.residual(r_in, y, post, f64(w_post), f64(gt), 0.5)
+    dz = dy
+    if post:
+        row = np.sqrt(np.mean(y * y, 1, keepdims=True))
+        dz = np.abs(f64(w_post)) * (dy + np.abs(y) * np.sqrt(np.mean(dy * dy, 1, keepdims=True)) / row) / row
+    got = f64(tail.r_out)
+    tol = 0.5 * np.abs(gg) * dz + np.abs(want) * (2.0 ** -8 if res == "bf16" else 1e-6) + 1e-6 * rms
+    err = np.abs(got - want)
+    assert np.all(err[clear] <= tol[clear]), np.max((err - tol)[clear])
+    nn = OB.rms_norm(got, f64(w_next))
+    assert np.all(np.abs(f64(n_next) - nn) <= np.abs(nn) * (2.0 ** -8 + 1e-5))
+
+
+def test_few_equals_forward_closely_on_a_decode_layer(moe):
+    """The same layer through moe_forward: equal up to FP8 codes of h that sit on a border."""
+    lay = make(dict(T=16, E=64, k=8, H=4096, I=2048))
+    p = problem(lay)
+    W, x, wr, ws = weights(lay, True), dev(lay["x"]), dev(lay["w_router"]), moe.alloc_block_workspace(p)
+    a, b = torch.empty(16, 4096, device="cuda"), torch.empty(16, 4096, device="cuda")
+    moe.forward_few(p, x, wr, None, W, a, ws)
+    moe.forward(p, x, wr, None, W, b, ws)
+    torch.cuda.synchronize()
+    rel = float((a - b).norm() / b.norm())
+    log("  few against forward: relative difference %.2e" % rel)
+    assert rel <= 2e-3
