@@ -38,8 +38,15 @@ extern "C" {
 
 /* Largest num_tokens of moe_forward_few: one 16-row MFMA tile per expert. */
 #define MOE_FEW_MAX_TOKENS 16
+/* Largest hidden and intermediate of moe_forward_few. */
+#define MOE_FEW_MAX_WIDTH 65536
 /* Largest hidden of the entry points of this header that take a norm. */
 #define MOE_BLOCK_MAX_HIDDEN 16384
+
+/* Bit of device error word 0 (moe_error_words_offset) after moe_forward_few or
+ * moe_block_forward: a wait inside the kernel was given up after seconds, and
+ * the call's results are unspecified.  No argument or data leads to it.     */
+#define MOE_DEVERR_STALLED 8
 
 /* What follows the layer.  Types are moe_out_dtype values (MOE_OUT_F32,
  * MOE_OUT_BF16).
@@ -89,18 +96,22 @@ moe_status moe_block_residual(const moe_problem* problem, const void* y, int32_t
 moe_status moe_combine_residual(const moe_problem* problem, const float* y_perm, const int32_t* row_of_slot,
                                 const float* topk_w, const moe_block_tail* tail, hipStream_t stream);
 
-/* The whole layer for num_tokens <= MOE_FEW_MAX_TOKENS (MOE_ERR_UNSUPPORTED
- * above): the computation of moe_forward with every rounding of its
- * definition (FP8 activations, FP8 h), in fewer launches.  Float32 sums are
- * taken in another order than moe_forward's.  workspace: at least
+/* The whole layer for num_tokens <= MOE_FEW_MAX_TOKENS, hidden and
+ * intermediate <= MOE_FEW_MAX_WIDTH (MOE_ERR_UNSUPPORTED above): the computation of moe_forward with every rounding of its
+ * definition (FP8 activations, FP8 h), in two launches.  Float32 sums are
+ * taken in another order than moe_forward's.  With FP8 block-scaled experts the
+ * activation and h scales are the float32 product amax * (1 / 448), at most an
+ * ulp from moe_forward's quotient (bf16 activations often lie on the border of
+ * two codes, so about one code in a thousand differs); codes are the e4m3
+ * rounding of v / scale as there.  workspace: at least
  * moe_block_workspace_size(problem) bytes, 256-byte aligned.               */
 moe_status moe_forward_few(const moe_problem* problem, const void* x_bf16, const void* w_router_bf16,
                            const float* sel_bias, const moe_expert_weights* weights, void* y, int32_t out_dtype,
                            void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* The block: n = RMSNorm(tail->r; w_pre), the layer on n, the tail.  w_pre is
- * [H] tail->param_dtype or NULL (= 1).  Any num_tokens; up to
- * MOE_FEW_MAX_TOKENS the layer runs as moe_forward_few.                    */
+ * [H] tail->param_dtype or NULL (= 1).  Any num_tokens; within
+ * the limits of moe_forward_few the layer runs as there.                   */
 moe_status moe_block_forward(const moe_problem* problem, const void* w_pre, const void* w_router_bf16,
                              const float* sel_bias, const moe_expert_weights* weights, const moe_block_tail* tail,
                              void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -215,7 +215,7 @@ def decode_fp8_block(codes, scales, block=FP8_BLOCK):
     return vals * np.repeat(np.repeat(sc, block, axis=0), block, axis=1)
 
 
-def quantize_fp8_blocks_f32(v, block=FP8_BLOCK):
+def quantize_fp8_blocks_f32(v, block=FP8_BLOCK, product=False):
     """Dynamic FP8 quantisation of rows with a float32 scale per row per `block` channels.
 
     The activation scheme that goes with FP8 block-scaled weights.  The pages
@@ -228,6 +228,8 @@ def quantize_fp8_blocks_f32(v, block=FP8_BLOCK):
              the quotient can exceed 448 by one binary32 rounding, and any
              such value rounds to 448).
     A run with amax == 0 stores s = 0 and the codes of v / 1 (signed zeros).
+    product=True (the layer for few tokens): s = amax * r with r = 1 / 448
+    rounded to binary32, one binary32 product.
 
     v: [R, C] (float64 or float32) with C % block == 0
     returns (codes [R, C] uint8, scales [R, C/block] float32)
@@ -238,7 +240,8 @@ def quantize_fp8_blocks_f32(v, block=FP8_BLOCK):
         raise ValueError("channel count must be a multiple of the block")
     blocks = v32.reshape(R, C // block, block)
     amax = np.abs(blocks).max(axis=-1)
-    s = (amax / np.float32(E4M3_MAX)).astype(np.float32)
+    top = np.float32(E4M3_MAX)
+    s = (amax * (np.float32(1.0) / top) if product else amax / top).astype(np.float32)
     div = np.where(amax > 0, s, np.float32(1.0)).astype(np.float32)
     q = (blocks / div[..., None]).astype(np.float32)
     q = np.clip(q, np.float32(-E4M3_MAX), np.float32(E4M3_MAX))

@@ -28,6 +28,11 @@ moe_status check_block_problem(const moe_problem* p) {
     return MOE_OK;
 }
 
+// Within the limits of moe_forward_few.
+bool few_supported(const moe_problem& p) {
+    return p.num_tokens <= kFewMaxT && p.hidden <= kFewMaxWidth && p.intermediate <= kFewMaxWidth;
+}
+
 struct Span { const void* p; size_t n; };
 
 // The tail's own fields, and that neither of its outputs overlaps an input
@@ -71,7 +76,12 @@ TailArgs tail_args(const moe_block_tail& t) {
 // moe_error_words_offset says), then the block's intermediates.
 struct BlockLayout {
     size_t layer, n, y, total;
+    // few_supported() only
+    size_t counters, logits, xq, xs, hq, hs, y_slot;
 };
+
+static_assert(kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH && kErrStalled == MOE_DEVERR_STALLED,
+              "constants of the kernels and of moe_block.h");
 
 BlockLayout block_layout(const moe_problem& p) {
     const size_t T = (size_t)p.num_tokens, H = (size_t)p.hidden;
@@ -81,6 +91,16 @@ BlockLayout block_layout(const moe_problem& p) {
     L.layer = take(moe_workspace_size(&p));
     L.n = take(T * H * 2);
     L.y = take(T * H * 4);
+    if (few_supported(p)) {
+        const size_t I = (size_t)p.intermediate, N = T * (size_t)p.top_k;
+        L.counters = take((size_t)few_counters(p.hidden) * 4);
+        L.logits = take(T * (size_t)p.num_experts * 4);
+        L.xq = take(T * H);
+        L.xs = take(T * (H / kFp8Block) * 4);
+        L.hq = take(N * I);
+        L.hs = take(N * (I / kFp8Block) * 4);
+        L.y_slot = take(N * H * 4);
+    }
     L.total = off;
     return L;
 }
@@ -88,6 +108,26 @@ BlockLayout block_layout(const moe_problem& p) {
 moe_status check_block_ws(const moe_problem& p, const void* ws, size_t ws_bytes) {
     if (!ws || ((uintptr_t)ws % kAlign) != 0) return MOE_ERR_INVALID_ARGUMENT;
     if (ws_bytes < block_layout(p).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return MOE_OK;
+}
+
+moe_status run_few(const moe_problem& p, const void* x, const void* w_router, const float* bias,
+                   const moe_expert_weights& w, void* y, bool out_bf16, void* ws, hipStream_t stream) {
+    const BlockLayout L = block_layout(p);
+    FewArgs a{};
+    a.x = (const uint16_t*)x; a.w_router = (const uint16_t*)w_router; a.bias = bias;
+    a.w13 = w.w13; a.w13_scale = w.w13_scale; a.w2 = w.w2; a.w2_scale = w.w2_scale;
+    a.y = y; a.out_bf16 = out_bf16;
+    a.T = (int)p.num_tokens; a.H = p.hidden; a.I = p.intermediate; a.E = p.num_experts; a.k = p.top_k;
+    a.sigmoid = p.score_func == MOE_SCORE_SIGMOID_BIAS;
+    a.err = at<uint32_t>(ws, moe_error_words_offset());
+    a.counters = at<uint32_t>(ws, L.counters);
+    a.n_counters = few_counters(p.hidden);
+    a.logits = at<float>(ws, L.logits);
+    a.xq = at<uint8_t>(ws, L.xq); a.xs = at<void>(ws, L.xs);
+    a.hq = at<uint8_t>(ws, L.hq); a.hs = at<void>(ws, L.hs);
+    a.y_slot = at<float>(ws, L.y_slot);
+    MOE_LAUNCH(launch_few_layer(a, w.layout == MOE_WEIGHTS_PACKED, p.expert_format == MOE_EXPERTS_FP8_BLOCK, stream));
     return MOE_OK;
 }
 
@@ -142,13 +182,13 @@ moe_status moe_forward_few(const moe_problem* p, const void* x_bf16, const void*
                            const moe_expert_weights* weights, void* y, int32_t out_dtype, void* ws, size_t ws_bytes,
                            hipStream_t stream) {
     MOE_CHECK(check_problem(p));
-    if (p->num_tokens > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+    if (!few_supported(*p)) return MOE_ERR_UNSUPPORTED;
     MOE_CHECK(check_weights(weights));
     if (!dtype_ok(out_dtype) || !all_aligned(x_bf16, w_router_bf16, y)) return MOE_ERR_INVALID_ARGUMENT;
     if (!opt_aligned(sel_bias)) return MOE_ERR_INVALID_ARGUMENT;
     MOE_CHECK(check_block_ws(*p, ws, ws_bytes));
     if (p->num_tokens == 0) return MOE_OK;
-    return moe_forward(p, x_bf16, w_router_bf16, sel_bias, weights, y, out_dtype, ws, ws_bytes, stream);
+    return run_few(*p, x_bf16, w_router_bf16, sel_bias, *weights, y, out_dtype == MOE_OUT_BF16, ws, stream);
 }
 
 moe_status moe_block_forward(const moe_problem* p, const void* w_pre, const void* w_router_bf16, const float* sel_bias,
@@ -169,7 +209,10 @@ moe_status moe_block_forward(const moe_problem* p, const void* w_pre, const void
     float* y = at<float>(ws, L.y);
     MOE_LAUNCH(launch_block_norm(tail->r, tail->res_dtype == MOE_OUT_BF16, w_pre, tail->param_dtype == MOE_OUT_BF16,
                                  tail->eps, n, p->num_tokens, p->hidden, stream));
-    MOE_CHECK(moe_forward(p, n, w_router_bf16, sel_bias, weights, y, MOE_OUT_F32, ws, ws_bytes, stream));
+    if (few_supported(*p))
+        MOE_CHECK(run_few(*p, n, w_router_bf16, sel_bias, *weights, y, false, ws, stream));
+    else
+        MOE_CHECK(moe_forward(p, n, w_router_bf16, sel_bias, weights, y, MOE_OUT_F32, ws, ws_bytes, stream));
     MOE_LAUNCH(launch_block_residual(y, 0, tail_args(*tail), p->num_tokens, p->hidden, stream));
     return MOE_OK;
 }

@@ -32,4 +32,41 @@ hipError_t launch_block_residual(const void* y, int y_bf16, const TailArgs& t, i
 hipError_t launch_combine_residual(const float* y_perm, const int32_t* row_of_slot, const float* w, const TailArgs& t,
                                    int64_t T, int H, int k, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// The layer for few tokens (few.hip).
+// ---------------------------------------------------------------------------
+constexpr int kFewMaxT = 16;              // tokens: one 16-row MFMA tile per expert
+constexpr int kFewMaxWidth = 65536;       // H and I: item counts and offsets inside an expert stay 32-bit
+constexpr int kFewCounterPad = 64;        // the ticket counter has 256 bytes to itself
+constexpr uint32_t kErrStalled = 8u;      // error word 0: a wait inside the kernel was given up
+
+// Counters of one call: the ticket, then per touched expert (at most 8 kFewMaxT)
+// the quantised 128-channel blocks of h, then the finished down items of each
+// 32 output features.
+inline int few_counters(int H) { return kFewCounterPad + 8 * kFewMaxT + H / 32; }
+
+struct FewArgs {
+    const uint16_t* x;          // [T][H] bf16
+    const uint16_t* w_router;   // [E][H] bf16
+    const float* bias;          // [E] or null
+    const uint8_t* w13;
+    const uint8_t* w13_scale;
+    const uint8_t* w2;
+    const uint8_t* w2_scale;
+    void* y;                    // [T][H] float32 or bf16
+    int out_bf16;
+    int T, H, I, E, k, sigmoid;
+    // workspace
+    uint32_t* err;              // two error words
+    uint32_t* counters;         // few_counters(H)
+    int n_counters;
+    float* logits;              // [T][E]
+    uint8_t* xq;                // [T][H] e4m3
+    void* xs;                   // [T][H / 128] e8m0 or float32
+    uint8_t* hq;                // [T k][I] e4m3
+    void* hs;                   // [T k][I / 128]
+    float* y_slot;              // [T k][H]
+};
+hipError_t launch_few_layer(const FewArgs& a, int packed, int fp8_block, hipStream_t stream);
+
 }  // namespace moe

@@ -1,22 +1,22 @@
-// FP8 quantisation of one bf16 row by one 256-thread workgroup, shared by the
-// quant-gather kernel and the decode router launch.
+// FP8 quantisation of one bf16 row by one workgroup of NT threads, shared by the
+// quant-gather kernel, the decode router launch and the layer for few tokens.
 //
 // 8 channels (one 16-byte bf16 load) per thread, so a 128-channel block is 16
 // consecutive lanes: amax by xor-shuffles within the 16, then the shared block
 // exponent, then RNE e4m3 codes of x * 2^-e (an exact power-of-two scaling).
 // F32S (FP8 block-scaled experts): the block's float32 scale amax / 448 and
-// RNE e4m3 codes of x / scale.
+// RNE e4m3 codes of x / scale (PRODUCT: the scale amax * (1 / 448)).
 #pragma once
 
 #include "moe_internal.h"
 
 namespace moe {
 
-template <bool F32S>
+template <bool F32S, int NT = 256, bool PRODUCT = false>
 __device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ xr, uint8_t* __restrict__ xq,
                                              void* __restrict__ xs, int r, int H) {
     uint8_t* qr = xq + (size_t)r * H;
-    for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
+    for (int c = threadIdx.x * 8; c < H; c += NT * 8) {
         const uint4 raw = *(const uint4*)(xr + c);
         float v[8];
         v[0] = bf16_bits_to_float(raw.x & 0xFFFFu); v[1] = bf16_bits_to_float(raw.x >> 16);
@@ -31,7 +31,7 @@ __device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ xr, ui
         float q[8];
         if constexpr (F32S) {
             // float32 scale amax / 448 (FP8 block-scaled experts)
-            const float sc = fp8_f32_scale(amax);
+            const float sc = PRODUCT ? fp8_f32_scale_product(amax) : fp8_f32_scale(amax);
             const float d = amax > 0.0f ? sc : 1.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = fp8_f32_quotient(v[i], d);

@@ -37,6 +37,9 @@ __device__ __forceinline__ int fp8_block_exponent(float amax) {
 // conversion away from its saturation path.  An all-zero block stores scale
 // 0 and divides by 1.
 __device__ __forceinline__ float fp8_f32_scale(float amax) { return amax / 448.0f; }
+// The same scale as a product with the reciprocal (at most an ulp away): the
+// rule of the layer for few tokens.
+__device__ __forceinline__ float fp8_f32_scale_product(float amax) { return amax * (1.0f / 448.0f); }
 __device__ __forceinline__ float fp8_f32_quotient(float v, float d) { return fminf(fmaxf(v / d, -448.0f), 448.0f); }
 
 // Four floats (already divided by their block scale, |v| <= 448) -> four

@@ -5,6 +5,7 @@
 // on the teardown page.
 #include "moe_internal.h"
 #include "fp8_rows.h"
+#include "topk_rows.h"
 
 #include <type_traits>
 
@@ -331,64 +332,8 @@ hipError_t launch_bias_update(const int32_t* offsets, int E, float step, float* 
 }
 
 // ---------------------------------------------------------------------------
-// Top-k selection + softmax weights: one wave per token.
-//
-// key = fp32(L + b).  Each key is mapped to an unsigned integer that orders
-// like the float (after -0 -> +0) and packed with ~id in the low word, so a
-// single 64-bit max picks the largest key and, among equal keys, the lowest
-// expert id.  k rounds of a wave-wide max; the winning lane retires its key.
-// Weights: softmax over the k selected *unbiased* logits, max-subtracted.
+// Top-k selection + combine weights: one wave per token (topk_rows.h).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t ordered_key(float f) {
-    if (f == 0.0f) f = 0.0f;   // -0 == +0
-    uint32_t u = __float_as_uint(f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// Largest value over the wave, returned wave-uniform: DPP shifts by 1, 2, 4
-// and 8 lanes leave each 16-lane row's maximum in its lane 15, two row
-// broadcasts (row 0 into row 1 and row 2 into row 3, then lane 31 into rows 2
-// and 3) carry the maxima to lane 63, and a readlane returns it.  DPP moves
-// stay in the VALU; a shuffle goes through LDS and costs far more latency.
-__device__ __forceinline__ uint32_t dpp_max_step(uint32_t v, uint32_t t) { return t > v ? t : v; }
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x111, 0xf, 0xf, false));   // row_shr:1
-    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x112, 0xf, 0xf, false));   // row_shr:2
-    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x114, 0xf, 0xf, false));   // row_shr:4
-    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x118, 0xf, 0xf, false));   // row_shr:8
-    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x142, 0xa, 0xf, false));   // row_bcast:15
-    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x143, 0xc, 0xf, false));   // row_bcast:31
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-// The same pattern for a float maximum and a float sum (lanes without a DPP
-// source add 0).
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ float dpp_f(float old, float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROW_MASK, 0xf, false));
-}
-__device__ __forceinline__ float wave_max_f32(float v) {
-    v = fmaxf(v, dpp_f<0x111, 0xf>(v, v));
-    v = fmaxf(v, dpp_f<0x112, 0xf>(v, v));
-    v = fmaxf(v, dpp_f<0x114, 0xf>(v, v));
-    v = fmaxf(v, dpp_f<0x118, 0xf>(v, v));
-    v = fmaxf(v, dpp_f<0x142, 0xa>(v, v));
-    v = fmaxf(v, dpp_f<0x143, 0xc>(v, v));
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-__device__ __forceinline__ float wave_sum_f32(float v) {
-    v += dpp_f<0x111, 0xf>(0.0f, v);
-    v += dpp_f<0x112, 0xf>(0.0f, v);
-    v += dpp_f<0x114, 0xf>(0.0f, v);
-    v += dpp_f<0x118, 0xf>(0.0f, v);
-    v += dpp_f<0x142, 0xa>(0.0f, v);
-    v += dpp_f<0x143, 0xc>(0.0f, v);
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-
-// SIG: sigmoid scoring (teardown "How Big Is Each Expert?": sigmoid expert
-// scores and a per-expert load-balancing bias):
-// key = fp32(sigmoid(L) + b), weights = sigmoid of the selected logits over
-// their sum.  Otherwise softmax scoring as above.
 template <int EJ, bool SIG>
 __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ logits,
                                                     const float* __restrict__ bias,
@@ -397,64 +342,13 @@ __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ log
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
-    const float* L = logits + (size_t)t * E;
-
-    float lv[EJ];
-    unsigned long long key[EJ];
-#pragma unroll
-    for (int j = 0; j < EJ; ++j) {
-        const int e = lane + 64 * j;
-        if (e < E) {
-            float l = L[e];
-            // the score replaces the logit: sigmoid evaluated in float64 and
-            // rounded once to float32, so that two implementations of it agree
-            // on the float32 score (and with it on the selection) unless the
-            // float64 value lies within an ulp or two of a float32 midpoint
-            if constexpr (SIG) l = (float)(1.0 / (1.0 + exp(-(double)l)));
-            float kf = bias ? l + bias[e] : l;
-            lv[j] = l;
-            key[j] = ((unsigned long long)ordered_key(kf) << 32) | (uint32_t)(~(uint32_t)e);
-        } else {
-            lv[j] = 0.0f;
-            key[j] = 0;
-        }
-    }
-
-    float sel = 0.0f;   // lane j (< k) keeps the j-th selected logit
-    int sid = 0;
-    for (int j = 0; j < k; ++j) {
-        unsigned long long best = 0;
-#pragma unroll
-        for (int q = 0; q < EJ; ++q) best = key[q] > best ? key[q] : best;
-        // the largest ordered key, then among the lanes holding it the
-        // largest ~id (the lowest expert id)
-        const uint32_t hi = wave_max_u32((uint32_t)(best >> 32));
-        const uint32_t lo = wave_max_u32((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
-        const int e = (int)(~lo);
-        const int owner = e & 63, slot = e >> 6;
-        float lsel = 0.0f;
-        if (lane == owner) {
-#pragma unroll
-            for (int q = 0; q < EJ; ++q)
-                if (q == slot) { key[q] = 0; lsel = lv[q]; }
-        }
-        lsel = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lsel), owner));
-        if (lane == j) { sel = lsel; sid = e; }
-    }
-
-    // softmax over the k selected logits held by lanes 0..k-1, or the
-    // selected sigmoid scores over their sum
-    float z;
-    if constexpr (SIG) {
-        z = lane < k ? sel : 0.0f;
-    } else {
-        const float m = wave_max_f32(lane < k ? sel : -__builtin_inff());
-        z = lane < k ? expf(sel - m) : 0.0f;
-    }
-    const float s = wave_sum_f32(z);
+    const float* const L[1] = {logits + (size_t)t * E};
+    int id[1];
+    float wt[1];
+    topk_rows<EJ, 1>(L, bias, E, k, SIG, id, wt);
     if (lane < k) {
-        ids[(size_t)t * k + lane] = sid;
-        w[(size_t)t * k + lane] = z / s;
+        ids[(size_t)t * k + lane] = id[0];
+        w[(size_t)t * k + lane] = wt[0];
     }
 }
 

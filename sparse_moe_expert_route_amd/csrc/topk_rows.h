@@ -1,0 +1,143 @@
+// Top-k selection and combine weights of N tokens by one wave, shared by the
+// router's top-k kernel and the layer for few tokens.
+//
+// key = fp32(L + b), mapped to an unsigned integer that orders like the float
+// (after -0 -> +0).  k rounds: the wave's largest key by DPP, then, of the lanes
+// and registers that hold it, the first in expert order (a ballot per register),
+// so that equal keys go to the lowest expert id; the winner retires its key.
+// Weights: softmax over the k selected *unbiased* logits, max-subtracted.
+// Several tokens share the rounds, whose dependent steps then overlap.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+__device__ __forceinline__ uint32_t ordered_key(float f) {
+    if (f == 0.0f) f = 0.0f;   // -0 == +0
+    uint32_t u = __float_as_uint(f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Largest value over the wave, returned wave-uniform: DPP shifts by 1, 2, 4
+// and 8 lanes leave each 16-lane row's maximum in its lane 15, two row
+// broadcasts (row 0 into row 1 and row 2 into row 3, then lane 31 into rows 2
+// and 3) carry the maxima to lane 63, and a readlane returns it.  DPP moves
+// stay in the VALU; a shuffle goes through LDS and costs far more latency.
+__device__ __forceinline__ uint32_t dpp_max_step(uint32_t v, uint32_t t) { return t > v ? t : v; }
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x111, 0xf, 0xf, false));   // row_shr:1
+    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x112, 0xf, 0xf, false));   // row_shr:2
+    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x114, 0xf, 0xf, false));   // row_shr:4
+    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x118, 0xf, 0xf, false));   // row_shr:8
+    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x142, 0xa, 0xf, false));   // row_bcast:15
+    v = dpp_max_step(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x143, 0xc, 0xf, false));   // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// The same pattern for a float maximum and a float sum (lanes without a DPP
+// source add 0).
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_f(float old, float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROW_MASK, 0xf, false));
+}
+__device__ __forceinline__ float wave_max_f32(float v) {
+    v = fmaxf(v, dpp_f<0x111, 0xf>(v, v));
+    v = fmaxf(v, dpp_f<0x112, 0xf>(v, v));
+    v = fmaxf(v, dpp_f<0x114, 0xf>(v, v));
+    v = fmaxf(v, dpp_f<0x118, 0xf>(v, v));
+    v = fmaxf(v, dpp_f<0x142, 0xa>(v, v));
+    v = fmaxf(v, dpp_f<0x143, 0xc>(v, v));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wave_sum_f32(float v) {
+    v += dpp_f<0x111, 0xf>(0.0f, v);
+    v += dpp_f<0x112, 0xf>(0.0f, v);
+    v += dpp_f<0x114, 0xf>(0.0f, v);
+    v += dpp_f<0x118, 0xf>(0.0f, v);
+    v += dpp_f<0x142, 0xa>(0.0f, v);
+    v += dpp_f<0x143, 0xc>(0.0f, v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// sig: sigmoid scoring (teardown "How Big Is Each Expert?": sigmoid expert
+// scores and a per-expert load-balancing bias): key = fp32(sigmoid(L) + b),
+// weights = sigmoid of the selected logits over their sum.  Otherwise softmax
+// scoring as above.
+// L[n]: token n's E logits, E <= 64 EJ.  Lane j < k returns the j-th selected
+// expert and its weight.
+template <int EJ, int N>
+__device__ __forceinline__ void topk_rows(const float* const (&L)[N], const float* __restrict__ bias, int E, int k,
+                                          bool sig, int (&id)[N], float (&w)[N]) {
+    const int lane = threadIdx.x & 63;
+    float lv[N][EJ];
+    uint32_t key[N][EJ];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int j = 0; j < EJ; ++j) lv[n][j] = lane + 64 * j < E ? L[n][lane + 64 * j] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < EJ; ++j) {
+        const int e = lane + 64 * j;
+        const float b = bias && e < E ? bias[e] : 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float l = lv[n][j];
+            // the score replaces the logit: sigmoid evaluated in float64 and
+            // rounded once to float32, so that two implementations of it agree
+            // on the float32 score (and with it on the selection) unless the
+            // float64 value lies within an ulp or two of a float32 midpoint
+            if (sig) l = (float)(1.0 / (1.0 + exp(-(double)l)));
+            lv[n][j] = l;
+            // 0 is a retired key or no expert
+            key[n][j] = e < E ? max(ordered_key(bias ? l + b : l), 1u) : 0u;
+        }
+    }
+
+    float sel[N];   // lane j (< k) keeps the j-th selected logit
+#pragma unroll
+    for (int n = 0; n < N; ++n) { sel[n] = 0.0f; id[n] = 0; }
+    for (int r = 0; r < k; ++r) {
+        uint32_t best[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            best[n] = key[n][0];
+#pragma unroll
+            for (int j = 1; j < EJ; ++j) best[n] = max(best[n], key[n][j]);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) best[n] = wave_max_u32(best[n]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            int e = -1;
+            float l = 0.0f;
+#pragma unroll
+            for (int j = EJ - 1; j >= 0; --j) {
+                const unsigned long long holds = __ballot(key[n][j] == best[n]);
+                if (holds) {
+                    const int owner = __builtin_ctzll(holds);
+                    e = 64 * j + owner;
+                    l = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lv[n][j]), owner));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < EJ; ++j) key[n][j] = e == lane + 64 * j ? 0u : key[n][j];
+            if (lane == r) { sel[n] = l; id[n] = e; }
+        }
+    }
+
+    // softmax over the k selected logits held by lanes 0..k-1, or the
+    // selected sigmoid scores over their sum
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float z;
+        if (sig) {
+            z = lane < k ? sel[n] : 0.0f;
+        } else {
+            const float m = wave_max_f32(lane < k ? sel[n] : -__builtin_inff());
+            z = lane < k ? expf(sel[n] - m) : 0.0f;
+        }
+        w[n] = z / wave_sum_f32(z);
+    }
+}
+
+}  // namespace moe

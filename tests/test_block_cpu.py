@@ -126,6 +126,7 @@ def test_few_refusals(lib):
     def few(p=None, x=M, wr=2 * M, b=None, w=None, y=3 * M, od=0, ws=64 * M, n=BIG):
         return lib.moe_forward_few(_P() if p is None else p, x, wr, b, _w() if w is None else w, y, od, ws, n, None)
     assert few(p=_P(T=17)) == UNSUPPORTED
+    assert few(p=_P(H=65536 + 128)) == UNSUPPORTED and few(p=_P(I=65536 + 128)) == UNSUPPORTED
     assert few(p=_P(H=200)) == INVALID and few(p=_P(sf=3)) == UNSUPPORTED
     assert few(x=None) == INVALID and few(wr=None) == INVALID and few(y=None) == INVALID
     assert few(x=M + 8) == INVALID and few(b=M + 4) == INVALID and few(y=M + 8) == INVALID

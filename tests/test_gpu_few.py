@@ -6,6 +6,8 @@ oracle flags as ambiguous, one step of an FP8 code of h carried through |W2|.  T
 lies within the float32 uncertainty of their logits of a tie are compared by nothing but finiteness.
 """
 
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -14,6 +16,7 @@ import synthetic as S
 from moe_testutil import (dev, host, log, weights, problem, unambiguous_tokens, key_margin, oracle_with_allowance,
                           check_output, bf16_rne, LOGIT_RTOL)
 from oracle import block as OB
+from oracle import formats as F
 from oracle import layer as OL
 
 pytestmark = pytest.mark.gpu
@@ -38,6 +41,12 @@ def make(over):
         b[np.random.default_rng(3).permutation(E)[:k]] = 100.0
         lay["bias"] = b
     return lay
+
+
+@pytest.fixture(autouse=True)
+def product_scales(monkeypatch):
+    """The FP8 block-scaled rule of the layer for few tokens: scale amax * (1 / 448)."""
+    monkeypatch.setattr(F, "quantize_fp8_blocks_f32", functools.partial(F.quantize_fp8_blocks_f32, product=True))
 
 
 def guarded(T, H, dtype):
