@@ -38,8 +38,11 @@ extern "C" {
 
 /* Largest num_tokens of moe_forward_few: one 16-row MFMA tile per expert. */
 #define MOE_FEW_MAX_TOKENS 16
-/* Largest hidden and intermediate of moe_forward_few. */
+/* Largest hidden and intermediate of moe_forward_few, and the largest
+ * num_tokens * (hidden + 16): the FP8 rows of x are kept in LDS (16 tokens up to
+ * hidden 7664, 14 at 8192, 7 at 16384). */
 #define MOE_FEW_MAX_WIDTH 65536
+#define MOE_FEW_MAX_ROW_BYTES 122880
 /* Largest hidden of the entry points of this header that take a norm. */
 #define MOE_BLOCK_MAX_HIDDEN 16384
 
@@ -96,8 +99,9 @@ moe_status moe_block_residual(const moe_problem* problem, const void* y, int32_t
 moe_status moe_combine_residual(const moe_problem* problem, const float* y_perm, const int32_t* row_of_slot,
                                 const float* topk_w, const moe_block_tail* tail, hipStream_t stream);
 
-/* The whole layer for num_tokens <= MOE_FEW_MAX_TOKENS, hidden and
- * intermediate <= MOE_FEW_MAX_WIDTH (MOE_ERR_UNSUPPORTED above): the computation of moe_forward with every rounding of its
+/* The whole layer for few tokens: num_tokens <= MOE_FEW_MAX_TOKENS, hidden and
+ * intermediate <= MOE_FEW_MAX_WIDTH and num_tokens * (hidden + 16) <=
+ * MOE_FEW_MAX_ROW_BYTES (MOE_ERR_UNSUPPORTED above): the computation of moe_forward with every rounding of its
  * definition (FP8 activations, FP8 h), in two launches.  Float32 sums are
  * taken in another order than moe_forward's.  With FP8 block-scaled experts the
  * activation and h scales are the float32 product amax * (1 / 448), at most an

@@ -30,7 +30,8 @@ moe_status check_block_problem(const moe_problem* p) {
 
 // Within the limits of moe_forward_few.
 bool few_supported(const moe_problem& p) {
-    return p.num_tokens <= kFewMaxT && p.hidden <= kFewMaxWidth && p.intermediate <= kFewMaxWidth;
+    return p.num_tokens <= kFewMaxT && p.hidden <= kFewMaxWidth && p.intermediate <= kFewMaxWidth &&
+           p.num_tokens * (p.hidden + 16) <= kFewRowBytes;
 }
 
 struct Span { const void* p; size_t n; };
@@ -80,7 +81,8 @@ struct BlockLayout {
     size_t counters, logits, xq, xs, hq, hs, y_slot;
 };
 
-static_assert(kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH && kErrStalled == MOE_DEVERR_STALLED,
+static_assert(kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH &&
+                  kFewRowBytes == MOE_FEW_MAX_ROW_BYTES && kErrStalled == MOE_DEVERR_STALLED,
               "constants of the kernels and of moe_block.h");
 
 BlockLayout block_layout(const moe_problem& p) {

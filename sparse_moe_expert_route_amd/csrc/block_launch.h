@@ -37,13 +37,16 @@ hipError_t launch_combine_residual(const float* y_perm, const int32_t* row_of_sl
 // ---------------------------------------------------------------------------
 constexpr int kFewMaxT = 16;              // tokens: one 16-row MFMA tile per expert
 constexpr int kFewMaxWidth = 65536;       // H and I: item counts and offsets inside an expert stay 32-bit
-constexpr int kFewCounterPad = 64;        // the ticket counter has 256 bytes to itself
+constexpr int kFewRowBytes = 122880;      // T (H + 16) at most: the FP8 rows of x in LDS
+constexpr int kFewCounterStride = 32;     // words between counters: each has its own 128-byte line
 constexpr uint32_t kErrStalled = 8u;      // error word 0: a wait inside the kernel was given up
 
 // Counters of one call: the ticket, then per touched expert (at most 8 kFewMaxT)
 // the quantised 128-channel blocks of h, then the finished down items of each
-// 32 output features.
-inline int few_counters(int H) { return kFewCounterPad + 8 * kFewMaxT + H / 32; }
+// 32 output features; behind them kFewPad words that stay zero (what the kernel
+// loads past the end of K).
+constexpr int kFewPad = 512;
+inline int few_counters(int H) { return kFewCounterStride * (1 + 8 * kFewMaxT + H / 32) + kFewPad; }
 
 struct FewArgs {
     const uint16_t* x;          // [T][H] bf16

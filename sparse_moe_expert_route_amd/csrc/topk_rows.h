@@ -75,10 +75,14 @@ __device__ __forceinline__ void topk_rows(const float* const (&L)[N], const floa
     for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int j = 0; j < EJ; ++j) lv[n][j] = lane + 64 * j < E ? L[n][lane + 64 * j] : 0.0f;
+    float bv[EJ];
+    if (bias) {
+#pragma unroll
+        for (int j = 0; j < EJ; ++j) bv[j] = lane + 64 * j < E ? bias[lane + 64 * j] : 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < EJ; ++j) {
         const int e = lane + 64 * j;
-        const float b = bias && e < E ? bias[e] : 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float l = lv[n][j];
@@ -89,7 +93,7 @@ __device__ __forceinline__ void topk_rows(const float* const (&L)[N], const floa
             if (sig) l = (float)(1.0 / (1.0 + exp(-(double)l)));
             lv[n][j] = l;
             // 0 is a retired key or no expert
-            key[n][j] = e < E ? max(ordered_key(bias ? l + b : l), 1u) : 0u;
+            key[n][j] = e < E ? max(ordered_key(bias ? l + bv[j] : l), 1u) : 0u;
         }
     }
 
