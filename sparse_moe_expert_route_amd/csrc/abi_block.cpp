@@ -96,7 +96,7 @@ BlockLayout block_layout(const moe_problem& p) {
     if (few_supported(p)) {
         const size_t I = (size_t)p.intermediate, N = T * (size_t)p.top_k;
         L.counters = take((size_t)few_counters(p.hidden) * 4);
-        L.logits = take(T * (size_t)p.num_experts * 4);
+        L.logits = take(kFewParts * T * (size_t)p.num_experts * 4);
         L.xq = take(T * H);
         L.xs = take(T * (H / kFp8Block) * 4);
         L.hq = take(N * I);
@@ -113,11 +113,22 @@ moe_status check_block_ws(const moe_problem& p, const void* ws, size_t ws_bytes)
     return MOE_OK;
 }
 
-moe_status run_few(const moe_problem& p, const void* x, const void* w_router, const float* bias,
-                   const moe_expert_weights& w, void* y, bool out_bf16, void* ws, hipStream_t stream) {
+// The layer for few tokens on x, or, with x null, the block on tail's residual
+// stream (y: workspace then).  The tail joins the layer's launch where a row fits
+// a wave's registers.
+moe_status run_few(const moe_problem& p, const void* x, const void* w_pre, const moe_block_tail* tail,
+                   const void* w_router, const float* bias, const moe_expert_weights& w, void* y, bool out_bf16,
+                   void* ws, hipStream_t stream) {
     const BlockLayout L = block_layout(p);
     FewArgs a{};
-    a.x = (const uint16_t*)x; a.w_router = (const uint16_t*)w_router; a.bias = bias;
+    a.x = (const uint16_t*)x;
+    if (!x) {
+        a.tail = tail_args(*tail);
+        a.r = tail->r;
+        a.w_pre = w_pre;
+        a.fuse_tail = p.hidden <= kFewTailMaxH;
+    }
+    a.w_router = (const uint16_t*)w_router; a.bias = bias;
     a.w13 = w.w13; a.w13_scale = w.w13_scale; a.w2 = w.w2; a.w2_scale = w.w2_scale;
     a.y = y; a.out_bf16 = out_bf16;
     a.T = (int)p.num_tokens; a.H = p.hidden; a.I = p.intermediate; a.E = p.num_experts; a.k = p.top_k;
@@ -130,6 +141,7 @@ moe_status run_few(const moe_problem& p, const void* x, const void* w_router, co
     a.hq = at<uint8_t>(ws, L.hq); a.hs = at<void>(ws, L.hs);
     a.y_slot = at<float>(ws, L.y_slot);
     MOE_LAUNCH(launch_few_layer(a, w.layout == MOE_WEIGHTS_PACKED, p.expert_format == MOE_EXPERTS_FP8_BLOCK, stream));
+    if (!x && !a.fuse_tail) MOE_LAUNCH(launch_block_residual(y, 0, a.tail, p.num_tokens, p.hidden, stream));
     return MOE_OK;
 }
 
@@ -190,7 +202,8 @@ moe_status moe_forward_few(const moe_problem* p, const void* x_bf16, const void*
     if (!opt_aligned(sel_bias)) return MOE_ERR_INVALID_ARGUMENT;
     MOE_CHECK(check_block_ws(*p, ws, ws_bytes));
     if (p->num_tokens == 0) return MOE_OK;
-    return run_few(*p, x_bf16, w_router_bf16, sel_bias, *weights, y, out_dtype == MOE_OUT_BF16, ws, stream);
+    return run_few(*p, x_bf16, nullptr, nullptr, w_router_bf16, sel_bias, *weights, y, out_dtype == MOE_OUT_BF16, ws,
+                   stream);
 }
 
 moe_status moe_block_forward(const moe_problem* p, const void* w_pre, const void* w_router_bf16, const float* sel_bias,
@@ -209,12 +222,11 @@ moe_status moe_block_forward(const moe_problem* p, const void* w_pre, const void
     const BlockLayout L = block_layout(*p);
     uint16_t* n = at<uint16_t>(ws, L.n);
     float* y = at<float>(ws, L.y);
+    if (few_supported(*p))
+        return run_few(*p, nullptr, w_pre, tail, w_router_bf16, sel_bias, *weights, y, false, ws, stream);
     MOE_LAUNCH(launch_block_norm(tail->r, tail->res_dtype == MOE_OUT_BF16, w_pre, tail->param_dtype == MOE_OUT_BF16,
                                  tail->eps, n, p->num_tokens, p->hidden, stream));
-    if (few_supported(*p))
-        MOE_CHECK(run_few(*p, n, w_router_bf16, sel_bias, *weights, y, false, ws, stream));
-    else
-        MOE_CHECK(moe_forward(p, n, w_router_bf16, sel_bias, weights, y, MOE_OUT_F32, ws, ws_bytes, stream));
+    MOE_CHECK(moe_forward(p, n, w_router_bf16, sel_bias, weights, y, MOE_OUT_F32, ws, ws_bytes, stream));
     MOE_LAUNCH(launch_block_residual(y, 0, tail_args(*tail), p->num_tokens, p->hidden, stream));
     return MOE_OK;
 }

@@ -38,32 +38,38 @@ hipError_t launch_combine_residual(const float* y_perm, const int32_t* row_of_sl
 constexpr int kFewMaxT = 16;              // tokens: one 16-row MFMA tile per expert
 constexpr int kFewMaxWidth = 65536;       // H and I: item counts and offsets inside an expert stay 32-bit
 constexpr int kFewRowBytes = 122880;      // T (H + 16) at most: the FP8 rows of x in LDS
+constexpr int kFewParts = 4;              // partial sums of a router logit
+constexpr int kFewTailMaxH = 8192;        // H of the tail in the layer's launch: a row in a wave's registers
 constexpr int kFewCounterStride = 32;     // words between counters: each has its own 128-byte line
 constexpr uint32_t kErrStalled = 8u;      // error word 0: a wait inside the kernel was given up
 
 // Counters of one call: the ticket, then per touched expert (at most 8 kFewMaxT)
 // the quantised 128-channel blocks of h, then the finished down items of each
-// 32 output features; behind them kFewPad words that stay zero (what the kernel
+// 32 output features, then the summed features; behind them kFewPad words that stay zero (what the kernel
 // loads past the end of K).
 constexpr int kFewPad = 512;
-inline int few_counters(int H) { return kFewCounterStride * (1 + 8 * kFewMaxT + H / 32) + kFewPad; }
+inline int few_counters(int H) { return kFewCounterStride * (2 + 8 * kFewMaxT + H / 32) + kFewPad; }
 
 struct FewArgs {
-    const uint16_t* x;          // [T][H] bf16
+    const uint16_t* x;          // [T][H] bf16 (null: the norm of r)
+    const void* r;              // [T][H] residual stream, tail.res_bf16, normalised with w_pre and tail.eps
+    const void* w_pre;          // [H] tail.param_bf16, or null (ones)
     const uint16_t* w_router;   // [E][H] bf16
     const float* bias;          // [E] or null
     const uint8_t* w13;
     const uint8_t* w13_scale;
     const uint8_t* w2;
     const uint8_t* w2_scale;
-    void* y;                    // [T][H] float32 or bf16
+    void* y;                    // [T][H] float32 or bf16 (fuse_tail: float32 workspace)
     int out_bf16;
+    int fuse_tail;              // the block's tail on y in the same launch
+    TailArgs tail;
     int T, H, I, E, k, sigmoid;
     // workspace
     uint32_t* err;              // two error words
     uint32_t* counters;         // few_counters(H)
     int n_counters;
-    float* logits;              // [T][E]
+    float* logits;              // [kFewParts][T][E]
     uint8_t* xq;                // [T][H] e4m3
     void* xs;                   // [T][H / 128] e8m0 or float32
     uint8_t* hq;                // [T k][I] e4m3

@@ -24,7 +24,10 @@
 //   - a down item loads its first weights, then waits until its expert's blocks
 //     are all counted;
 //   - the wave whose down item is the last on its 32 features (one from every
-//     touched expert) sums them over the k slots of every token, in slot order.
+//     touched expert) sums them over the k slots of every token, in slot order;
+//   - in the block's form (moe_block_forward) the items after the last down item
+//     are the rows of the residual stream: a wave waits until all of y is summed
+//     and does gate, residual sum and norms of one row.
 // Which wave does that depends on timing, what it computes does not: results
 // have the same bits on every run.
 //
@@ -44,6 +47,7 @@
 #include <type_traits>
 
 #include "block_launch.h"
+#include "block_rows.h"
 #include "moe_internal.h"
 #include "fp8_rows.h"
 #include "topk_rows.h"
@@ -52,15 +56,12 @@ namespace moe {
 
 namespace {
 
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef int v4i __attribute__((ext_vector_type(4)));
-
 constexpr int kFewWaves = 8;                  // waves per workgroup of the layer kernel
 constexpr int kFewPlaces = 4;                 // runs a workgroup can have in work
 constexpr int kFewGrid = 256;                 // its workgroups: one per CU
 constexpr int kFewSlots = kFewMaxT * 8;       // routing slots, and so touched experts, at most
 constexpr uint32_t kFewMaxPolls = 1u << 23;
-constexpr int kRouteWaves = 16;               // waves per workgroup of the route kernel
+constexpr int kRouteWaves = 8;                // waves per workgroup of the route kernel
 
 // ---- agent-scope accesses and counters ------------------------------------
 __device__ __forceinline__ void put8(void* p, uint32_t lo, uint32_t hi) {
@@ -91,53 +92,114 @@ __device__ __forceinline__ uint32_t count(uint32_t* c) {
     return v;
 }
 // ---------------------------------------------------------------------------
-// Route kernel.  Workgroups of 16 waves:
-//   [0, gx)        router logits of 16 experts x 16 tokens on the bf16 MFMA, the
-//                  16 waves splitting K (H = 4096: 8 steps each, all loads of a
-//                  wave in flight at once), summed through LDS in wave order;
-//   [gx, gx + T)   the FP8 copy of one token row;
-//   gx + T         the counters and error words of the layer kernel, cleared.
+// Route kernel.  Workgroups of 8 waves:
+//   [0, gx kFewParts)   router logits of 16 experts x 16 tokens over a quarter of
+//                       K on the bf16 MFMA, the 8 waves splitting it again (H =
+//                       4096: 4 steps each, all loads of a wave in flight at
+//                       once), summed through LDS in wave order.  The quarters
+//                       are summed, in order, by the layer kernel.  (Whole
+//                       rows in 16 or 24 workgroups waited on the few CUs'
+//                       own load paths: 17 us for 16 tokens of the Pro layer.)
+//   the next T          the FP8 copy of one token row;
+//   the last            the counters and error words of the layer kernel, cleared.
+// SRC: what the rows are made of: 0 the layer's input x (bf16); 1, 2 the
+// residual stream (bf16, float32), normalised here: every workgroup that needs
+// rows takes their sums of squares itself (they are a few 8 to 24 KB rows in the
+// L2), which spares the block its own norm launch.
 // ---------------------------------------------------------------------------
-template <bool F32S>
+enum RowSource { kRowsX = 0, kRowsBf16 = 1, kRowsF32 = 2 };
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
+// 8 channels at c of row t of the layer's input
+template <int SRC>
+__device__ __forceinline__ v8bf input8(const FewArgs& a, int t, int c, float rstd) {
+    const size_t o = (size_t)t * a.H + c;
+    if constexpr (SRC == kRowsX) {
+        return *(const v8bf*)(a.x + o);
+    } else {
+        float v[8];
+        load8<false>(a.r, SRC == kRowsBf16, o, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= rstd;
+        if (a.w_pre) {
+            float w[8];
+            load8<false>(a.w_pre, a.tail.param_bf16, c, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= w[i];
+        }
+        return __builtin_bit_cast(v8bf, pack8(v));
+    }
+}
+
+// sum of squares of row t over a wave
+template <int SRC>
+__device__ __forceinline__ float row_squares(const FewArgs& a, int t, int first, int step) {
+    float s = 0.0f;
+#pragma unroll 4
+    for (int c = first * 8; c < a.H; c += step * 8) {
+        float v[8];
+        load8<false>(a.r, SRC == kRowsBf16, (size_t)t * a.H + c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+    }
+    return wave_sum(s);
+}
+
+template <bool F32S, int SRC>
 __global__ void __launch_bounds__(64 * kRouteWaves) few_route_kernel(FewArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int gx = (a.E + 15) / 16;
+    const int gx = (a.E + 15) / 16 * kFewParts;
     const int b = blockIdx.x;
     if (b >= gx + a.T) {
         for (int i = tid; i < a.n_counters; i += 64 * kRouteWaves) a.counters[i] = 0u;
         if (tid < 2) a.err[tid] = 0u;
         return;
     }
+    __shared__ float squares[kFewMaxT];
+    __shared__ v4f red[kRouteWaves][64];
     if (b >= gx) {
-        quantise_row<F32S, 64 * kRouteWaves, true>(a.x + (size_t)(b - gx) * a.H, a.xq, a.xs, b - gx, a.H);
+        const int t = b - gx;
+        float rstd = 1.0f;
+        if constexpr (SRC != kRowsX) {
+            const float s = row_squares<SRC>(a, t, tid, 64 * kRouteWaves);
+            if (lane == 0) squares[wave] = s;
+            __syncthreads();
+            float v = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kRouteWaves; ++q) v += squares[q];
+            rstd = inv_rms(v, a.H, a.tail.eps);
+        }
+        quantise_channels<F32S, 64 * kRouteWaves, true>([&](int c) { return __builtin_bit_cast(uint4, input8<SRC>(a, t, c, rstd)); },
+                                                       a.xq, a.xs, t, a.H);
         return;
     }
-    __shared__ v4f red[kRouteWaves][64];
-    const int g = lane >> 4, r = lane & 15, e0 = 16 * b;
+    const int g = lane >> 4, r = lane & 15, e0 = b / kFewParts * 16;
+    const int t = min(r, a.T - 1);
     const uint16_t* wp = a.w_router + (size_t)min(e0 + r, a.E - 1) * a.H + 8 * g;
-    const uint16_t* xp = a.x + (size_t)min(r, a.T - 1) * a.H + 8 * g;
-    const int ns = a.H / 32;
-    const int s0 = wave * ns / kRouteWaves, s1 = (wave + 1) * ns / kRouteWaves;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    constexpr int U = 8;
-    int s = s0;
-    for (; s + U <= s1; s += U) {
-        v8bf wa[U], xb[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            wa[u] = *(const v8bf*)(wp + 32 * (s + u));
-            xb[u] = *(const v8bf*)(xp + 32 * (s + u));
+    const int ns = a.H / 32, q = b % kFewParts * kRouteWaves + wave;
+    const int s0 = q * ns / (kFewParts * kRouteWaves), s1 = (q + 1) * ns / (kFewParts * kRouteWaves);
+    float rstd = 1.0f;
+    if constexpr (SRC != kRowsX) {
+        for (int u = wave; u < a.T; u += kRouteWaves) {
+            const float s = row_squares<SRC>(a, u, lane, 64);
+            if (lane == 0) squares[u] = s;
         }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa[u], xb[u], acc, 0, 0, 0);
+        __syncthreads();
+        rstd = inv_rms(squares[t], a.H, a.tail.eps);
     }
-    if (s < s1) {   // the last, shorter chunk: past its end the last step is loaded again and left out
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 6;
+    for (int s = s0; s < s1; s += U) {   // past the end: the last step again, left out
         v8bf wa[U], xb[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             wa[u] = *(const v8bf*)(wp + 32 * min(s + u, s1 - 1));
-            xb[u] = *(const v8bf*)(xp + 32 * min(s + u, s1 - 1));
+            xb[u] = input8<SRC>(a, t, 32 * min(s + u, s1 - 1) + 8 * g, rstd);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -151,9 +213,9 @@ __global__ void __launch_bounds__(64 * kRouteWaves) few_route_kernel(FewArgs a) 
         const int l = tid >> 2, i = tid & 3;
         float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kRouteWaves; ++q) v += red[q][l][i];
-        const int e = e0 + 4 * (l >> 4) + i, t = l & 15;
-        if (e < a.E && t < a.T) a.logits[(size_t)t * a.E + e] = v;
+        for (int w = 0; w < kRouteWaves; ++w) v += red[w][l][i];
+        const int e = e0 + 4 * (l >> 4) + i, tt = l & 15;
+        if (e < a.E && tt < a.T) a.logits[((size_t)(b % kFewParts) * a.T + tt) * a.E + e] = v;
     }
 }
 
@@ -513,6 +575,7 @@ struct FewPlan {
     uint32_t finished[kFewPlaces];           // gate/up items whose h is in the place
     uint32_t freed[kFewPlaces];              // the place's runs that are over
     uint32_t ready[kFewSlots];               // experts whose h is known to be there
+    uint32_t summed;                         // all of y is known to be there
     uint32_t polling;                        // a wave is asking memory
     unsigned long long run[kFewPlaces];      // (c + 1) << 32 | number of run c
     float h[kFewPlaces][kFewMaxT][kFp8Block + 4];   // h of a gate/up run: rows of 128 channels
@@ -527,19 +590,20 @@ __device__ __forceinline__ uint32_t next_run(uint32_t* ticket) {
     return __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Waits until expert u's KBI blocks of h are there.  One wave of the workgroup at
-// a time asks memory (polls of one address leave it one after the other, and the
-// counts that they wait for queue behind them); the others look at LDS.
-__device__ __forceinline__ void wait_ready(const FewArgs& a, FewPlan& s, const uint32_t* ready, int u, uint32_t KBI) {
-    for (uint32_t i = 0; !lds_load(&s.ready[u]); ++i) {
+// Waits until *c >= n; `known`, in LDS, says that a wave has seen it.  One wave of
+// the workgroup at a time asks memory (polls of one address leave it one after
+// the other, and the counts that they wait for queue behind them); the others
+// look at LDS.
+__device__ __forceinline__ void wait_for(const FewArgs& a, FewPlan& s, const uint32_t* c, uint32_t n, uint32_t* known) {
+    for (uint32_t i = 0; !lds_load(known); ++i) {
         uint32_t v = 0;
         if ((threadIdx.x & 63) == 0 && __hip_atomic_exchange(&s.polling, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) == 0) {
-            v = __hip_atomic_load(ready + u * kFewCounterStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (v >= KBI || i >= kFewMaxPolls) __hip_atomic_store(&s.ready[u], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-            if (v < KBI && i >= kFewMaxPolls) __hip_atomic_store(a.err, kErrStalled, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (v >= n || i >= kFewMaxPolls) __hip_atomic_store(known, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            if (v < n && i >= kFewMaxPolls) __hip_atomic_store(a.err, kErrStalled, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             __hip_atomic_store(&s.polling, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
-        if (uniform((int)v) >= (int)KBI) break;
+        if ((uint32_t)uniform((int)v) >= n) break;
         __builtin_amdgcn_s_sleep(8);
     }
     asm volatile("" ::: "memory");
@@ -568,14 +632,14 @@ __device__ __forceinline__ int draw(uint32_t* ticket, FewPlan& s, int& place) {
 }
 
 template <int EJ>
-__device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s) {
+__device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s, uint8_t* x_rows, uint32_t pitch) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     static_assert(64 * kFewWaves == 512, "one thread per expert");
     static_assert(kFewMaxT <= 2 * kFewWaves, "two tokens per wave");
     s.mask[tid] = 0;
     if (tid < kFewPlaces) { s.read[tid] = 0; s.finished[tid] = 0; s.freed[tid] = 0; s.run[tid] = 0; }
     if (tid < kFewSlots) s.ready[tid] = 0;
-    if (tid == 0) { s.drawn = 0; s.polling = 0; }
+    if (tid == 0) { s.drawn = 0; s.summed = 0; s.polling = 0; }
     __syncthreads();
     // the first run, while the others wait for the logits
     if (tid == 64 * kFewWaves - 1) s.run[0] = (1ull << 32) | next_run(a.counters);
@@ -590,15 +654,22 @@ __device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s) {
         const float* const L[2] = {a.logits + (size_t)wave * a.E, a.logits + (size_t)(wave + kFewWaves) * a.E};
         int id[2];
         float w[2];
-        topk_rows<EJ, 2>(L, a.bias, a.E, a.k, a.sigmoid, id, w);
+        topk_rows<EJ, 2, kFewParts>(L, a.bias, a.E, a.k, a.sigmoid, id, w, (size_t)a.T * a.E);
         token(wave, id[0], w[0]);
         token(wave + kFewWaves, id[1], w[1]);
     } else if (wave < a.T) {
         const float* const L[1] = {a.logits + (size_t)wave * a.E};
         int id[1];
         float w[1];
-        topk_rows<EJ, 1>(L, a.bias, a.E, a.k, a.sigmoid, id, w);
+        topk_rows<EJ, 1, kFewParts>(L, a.bias, a.E, a.k, a.sigmoid, id, w, (size_t)a.T * a.E);
         token(wave, id[0], w[0]);
+    }
+    // the rows of x, behind the top-k of the waves that have tokens
+    const int pieces = a.H / 16;
+#pragma unroll 4
+    for (int i = tid; i < a.T * pieces; i += 64 * kFewWaves) {
+        const int t = i / pieces, c = i - t * pieces;
+        *(uint4*)(x_rows + t * pitch + 16 * c) = *(const uint4*)(a.xq + (size_t)t * a.H + 16 * c);
     }
     __syncthreads();
     const uint32_t m = s.mask[tid];
@@ -688,13 +759,89 @@ __device__ __forceinline__ void combine_block(const FewArgs& a, const FewPlan& s
                 acc[3] = fmaf(w, __uint_as_float(p[j].w), acc[3]);
             }
         }
-        if (a.out_bf16) {
+        if (a.fuse_tail) {
+            put16((float*)a.y + (size_t)t * a.H + c, acc);
+        } else if (a.out_bf16) {
             uint2 o;
             o.x = (uint32_t)float_to_bf16_rne(acc[0]) | ((uint32_t)float_to_bf16_rne(acc[1]) << 16);
             o.y = (uint32_t)float_to_bf16_rne(acc[2]) | ((uint32_t)float_to_bf16_rne(acc[3]) << 16);
             *(uint2*)((uint16_t*)a.y + (size_t)t * a.H + c) = o;
         } else {
             *(v4f*)((float*)a.y + (size_t)t * a.H + c) = acc;
+        }
+    }
+}
+
+// The block's tail on row t of y, by one wave: gate, residual sum and norms as in
+// block_norm.hip.  H <= kFewTailMaxH.
+__device__ __forceinline__ void tail_row(const FewArgs& a, int t) {
+    constexpr int V = kFewTailMaxH / 512;   // pieces of 8 channels per lane
+    const int lane = threadIdx.x & 63;
+    const TailArgs& T = a.tail;
+    const size_t row = (size_t)t * a.H;
+    float v[V][8];
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int c = (64 * u + lane) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+        if (c < a.H) {
+            const uint4 p0 = get16((const float*)a.y + row + c), p1 = get16((const float*)a.y + row + c + 4);
+            const uint32_t b[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = __uint_as_float(b[i]);
+        }
+    }
+    auto rstd = [&]() {
+        float s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(v[u][i], v[u][i], s);
+        return inv_rms(wave_sum(s), a.H, T.eps);
+    };
+    auto times = [&](const void* w, size_t o, float (&x)[8]) {
+        float f[8];
+        load8<false>(w, T.param_bf16, o, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= f[i];
+    };
+    const float post = T.post_norm ? rstd() : 1.0f;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int c = (64 * u + lane) * 8;
+        if (c < a.H) {
+            if (T.post_norm) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= post;
+                if (T.w_post) times(T.w_post, c, v[u]);
+            }
+            if (T.gate) times(T.gate, (T.gate_per_token ? row : 0) + c, v[u]);
+            float r[8];
+            load8<false>(T.r, T.res_bf16, row + c, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] = fmaf(T.scale, v[u][i], r[i]);
+            if (T.res_bf16) {
+                const v4u o = pack8(v[u]);
+                *(v4u*)((uint16_t*)T.r_out + row + c) = o;
+                unpack8(o, v[u]);   // n' is the norm of r' as stored
+            } else {
+                v4f* o = (v4f*)((float*)T.r_out + row + c);
+                o[0] = v4f{v[u][0], v[u][1], v[u][2], v[u][3]};
+                o[1] = v4f{v[u][4], v[u][5], v[u][6], v[u][7]};
+            }
+        }
+    }
+    if (!T.n_next) return;
+    const float next = rstd();
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int c = (64 * u + lane) * 8;
+        if (c < a.H) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[u][i] *= next;
+            if (T.w_next) times(T.w_next, c, v[u]);
+            *(v4u*)((uint16_t*)T.n_next + row + c) = pack8(v[u]);
         }
     }
 }
@@ -706,20 +853,18 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     // lie on different banks
     __shared__ __attribute__((aligned(16))) uint8_t x_rows[kFewRowBytes];
     const uint32_t pitch = a.H + 16;
-    for (int i = threadIdx.x; i < a.T * (a.H / 16); i += 64 * kFewWaves) {
-        const int t = i / (a.H / 16), c = i - t * (a.H / 16);
-        *(uint4*)(x_rows + t * pitch + 16 * c) = *(const uint4*)(a.xq + (size_t)t * a.H + 16 * c);
-    }
-    const int U = few_plan<EJ>(a, s);
+    const int U = few_plan<EJ>(a, s, x_rows, pitch);
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int KBI = a.I / kFp8Block;
     uint32_t* ticket = a.counters;
     uint32_t* ready = a.counters + kFewCounterStride;                     // [U] quantised blocks
     uint32_t* fb_count = ready + kFewSlots * kFewCounterStride;           // [H / 32] down items
     const int f2 = a.H / 32;
-    const uint8_t* pad = (const uint8_t*)(fb_count + f2 * kFewCounterStride);   // kFewPad words of zeros
+    uint32_t* done = fb_count + f2 * kFewCounterStride;                   // summed features of y, in 32s
+    const uint8_t* pad = (const uint8_t*)(done + kFewCounterStride);      // kFewPad words of zeros
     const int f1 = a.I / 16, n1 = U * f1;                                 // gate/up items (runs: 128-channel blocks)
     const int n2 = U * f2;                                                // down items
+    const int n3 = (n2 + kFewWaves - 1) / kFewWaves * kFewWaves;          // first item behind their runs
     const uint32_t xs_row = (a.H / kFp8Block) * (FMT == 1 ? 4 : 1), hs_row = KBI * (FMT == 1 ? 4 : 1);
 
     int place;
@@ -788,14 +933,29 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     };
     auto finish = [&](int f) {
         wave_done();
-        if (count(fb_count + f * kFewCounterStride) == (uint32_t)(U - 1)) combine_block(a, s, f);
+        if (count(fb_count + f * kFewCounterStride) == (uint32_t)(U - 1)) {
+            combine_block(a, s, f);
+            if (a.fuse_tail) {
+                wave_done();
+                count(done);
+            }
+        }
+    };
+    // a wave's next item, the rest of the last down run left out: every wave then
+    // ends with one item >= n3, and a workgroup's 8 waves with one whole run of them
+    auto draw_down = [&]() {
+        int i;
+        do i = draw(ticket, s, place) - n1;
+        while (i >= n2 && i < n3);
+        return i;
     };
     item -= n1;
+    if (item >= n2 && item < n3) item = draw_down();
     int stored = -1;   // features whose rows are stored, not yet counted
     Item it;
     if (item < n2) begin(item, it);
     while (item < n2) {
-        wait_ready(a, s, ready, it.u, (uint32_t)KBI);
+        wait_for(a, s, ready + it.u * kFewCounterStride, (uint32_t)KBI, &s.ready[it.u]);
         if (stored >= 0) finish(stored);
         v4f acc[2];
         down_item<FMT, PK>(it.P, w, acc);
@@ -805,10 +965,15 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
             put16(o + 16, acc[1]);
         }
         stored = it.f;
-        item = draw(ticket, s, place) - n1;
+        item = draw_down();
         if (item < n2) begin(item, it);
     }
     if (stored >= 0) finish(stored);
+    // The block's tail: behind the down items there is one for each row.
+    if (a.fuse_tail && item < n3 + a.T) {
+        wait_for(a, s, done, (uint32_t)f2, &s.summed);
+        tail_row(a, item - n3);
+    }
 }
 
 template <int FMT, bool PK>
@@ -819,14 +984,22 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <bool F32S>
+hipError_t launch_route(const FewArgs& a, hipStream_t stream) {
+    const dim3 grid((a.E + 15) / 16 * kFewParts + a.T + 1), block(64 * kRouteWaves);
+    if (!a.r) hipLaunchKernelGGL((few_route_kernel<F32S, kRowsX>), grid, block, 0, stream, a);
+    else if (a.tail.res_bf16) hipLaunchKernelGGL((few_route_kernel<F32S, kRowsBf16>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((few_route_kernel<F32S, kRowsF32>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_few_layer(const FewArgs& a, int packed, int fp8_block, hipStream_t stream) {
-    if (a.T < 1 || a.T > kFewMaxT || a.T * (a.H + 16) > kFewRowBytes || a.n_counters < few_counters(a.H)) return hipErrorInvalidValue;
-    const dim3 grid((a.E + 15) / 16 + a.T + 1), block(64 * kRouteWaves);
-    if (fp8_block) hipLaunchKernelGGL(few_route_kernel<true>, grid, block, 0, stream, a);
-    else hipLaunchKernelGGL(few_route_kernel<false>, grid, block, 0, stream, a);
-    const hipError_t st = hipGetLastError();
+    if (a.T < 1 || a.T > kFewMaxT || a.T * (a.H + 16) > kFewRowBytes || a.n_counters < few_counters(a.H))
+        return hipErrorInvalidValue;
+    if (a.fuse_tail && a.H > kFewTailMaxH) return hipErrorInvalidValue;
+    const hipError_t st = fp8_block ? launch_route<true>(a, stream) : launch_route<false>(a, stream);
     if (st != hipSuccess) return st;
     if (fp8_block) return packed ? launch_layer<1, true>(a, stream) : launch_layer<1, false>(a, stream);
     return packed ? launch_layer<0, true>(a, stream) : launch_layer<2, false>(a, stream);

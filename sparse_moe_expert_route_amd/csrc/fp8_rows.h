@@ -12,12 +12,13 @@
 
 namespace moe {
 
-template <bool F32S, int NT = 256, bool PRODUCT = false>
-__device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ xr, uint8_t* __restrict__ xq,
-                                             void* __restrict__ xs, int r, int H) {
+// load(c): the row's 8 bf16 channels from c
+template <bool F32S, int NT, bool PRODUCT, typename Load>
+__device__ __forceinline__ void quantise_channels(Load load, uint8_t* __restrict__ xq, void* __restrict__ xs, int r,
+                                                  int H) {
     uint8_t* qr = xq + (size_t)r * H;
     for (int c = threadIdx.x * 8; c < H; c += NT * 8) {
-        const uint4 raw = *(const uint4*)(xr + c);
+        const uint4 raw = load(c);
         float v[8];
         v[0] = bf16_bits_to_float(raw.x & 0xFFFFu); v[1] = bf16_bits_to_float(raw.x >> 16);
         v[2] = bf16_bits_to_float(raw.y & 0xFFFFu); v[3] = bf16_bits_to_float(raw.y >> 16);
@@ -47,6 +48,12 @@ __device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ xr, ui
         codes.y = pack_fp8x4(q[4], q[5], q[6], q[7]);
         *(uint2*)(qr + c) = codes;
     }
+}
+
+template <bool F32S>
+__device__ __forceinline__ void quantise_row(const uint16_t* __restrict__ xr, uint8_t* __restrict__ xq,
+                                             void* __restrict__ xs, int r, int H) {
+    quantise_channels<F32S, 256, false>([&](int c) { return *(const uint4*)(xr + c); }, xq, xs, r, H);
 }
 
 }  // namespace moe

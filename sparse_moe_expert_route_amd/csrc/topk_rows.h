@@ -63,22 +63,27 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 // scores and a per-expert load-balancing bias): key = fp32(sigmoid(L) + b),
 // weights = sigmoid of the selected logits over their sum.  Otherwise softmax
 // scoring as above.
-// L[n]: token n's E logits, E <= 64 EJ.  Lane j < k returns the j-th selected
-// expert and its weight.
-template <int EJ, int N>
+// L[n]: token n's E logits, E <= 64 EJ, each the sum of PARTS values `stride`
+// apart.  Lane j < k returns the j-th selected expert and its weight.
+template <int EJ, int N, int PARTS = 1>
 __device__ __forceinline__ void topk_rows(const float* const (&L)[N], const float* __restrict__ bias, int E, int k,
-                                          bool sig, int (&id)[N], float (&w)[N]) {
+                                          bool sig, int (&id)[N], float (&w)[N], size_t stride = 0) {
     const int lane = threadIdx.x & 63;
     float lv[N][EJ];
     uint32_t key[N][EJ];
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int j = 0; j < EJ; ++j) lv[n][j] = lane + 64 * j < E ? L[n][lane + 64 * j] : 0.0f;
+        for (int j = 0; j < EJ; ++j) {
+            const float* p = L[n] + min(lane + 64 * j, E - 1);
+            lv[n][j] = p[0];
+#pragma unroll
+            for (int q = 1; q < PARTS; ++q) lv[n][j] += p[q * stride];
+        }
     float bv[EJ];
     if (bias) {
 #pragma unroll
-        for (int j = 0; j < EJ; ++j) bv[j] = lane + 64 * j < E ? bias[lane + 64 * j] : 0.0f;
+        for (int j = 0; j < EJ; ++j) bv[j] = bias[min(lane + 64 * j, E - 1)];
     }
 #pragma unroll
     for (int j = 0; j < EJ; ++j) {
