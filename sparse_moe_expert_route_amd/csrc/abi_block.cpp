@@ -81,7 +81,7 @@ struct BlockLayout {
     size_t counters, logits, xq, xs, hq, hs, y_slot;
 };
 
-static_assert(kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH &&
+static_assert(kFewTailMaxH == MOE_BLOCK_MAX_HIDDEN && kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH &&
                   kFewRowBytes == MOE_FEW_MAX_ROW_BYTES && kErrStalled == MOE_DEVERR_STALLED,
               "constants of the kernels and of moe_block.h");
 
@@ -126,7 +126,7 @@ moe_status run_few(const moe_problem& p, const void* x, const void* w_pre, const
         a.tail = tail_args(*tail);
         a.r = tail->r;
         a.w_pre = w_pre;
-        a.fuse_tail = p.hidden <= kFewTailMaxH;
+        a.fuse_tail = 1;
     }
     a.w_router = (const uint16_t*)w_router; a.bias = bias;
     a.w13 = w.w13; a.w13_scale = w.w13_scale; a.w2 = w.w2; a.w2_scale = w.w2_scale;
@@ -141,7 +141,6 @@ moe_status run_few(const moe_problem& p, const void* x, const void* w_pre, const
     a.hq = at<uint8_t>(ws, L.hq); a.hs = at<void>(ws, L.hs);
     a.y_slot = at<float>(ws, L.y_slot);
     MOE_LAUNCH(launch_few_layer(a, w.layout == MOE_WEIGHTS_PACKED, p.expert_format == MOE_EXPERTS_FP8_BLOCK, stream));
-    if (!x && !a.fuse_tail) MOE_LAUNCH(launch_block_residual(y, 0, a.tail, p.num_tokens, p.hidden, stream));
     return MOE_OK;
 }
 

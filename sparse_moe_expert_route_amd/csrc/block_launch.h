@@ -39,7 +39,7 @@ constexpr int kFewMaxT = 16;              // tokens: one 16-row MFMA tile per ex
 constexpr int kFewMaxWidth = 65536;       // H and I: item counts and offsets inside an expert stay 32-bit
 constexpr int kFewRowBytes = 122880;      // T (H + 16) at most: the FP8 rows of x in LDS
 constexpr int kFewParts = 4;              // partial sums of a router logit
-constexpr int kFewTailMaxH = 8192;        // H of the tail in the layer's launch: a row in a wave's registers
+constexpr int kFewTailMaxH = 16384;       // H of the block: a row of the tail in a workgroup's registers
 constexpr int kFewCounterStride = 32;     // words between counters: each has its own 128-byte line
 constexpr uint32_t kErrStalled = 8u;      // error word 0: a wait inside the kernel was given up
 

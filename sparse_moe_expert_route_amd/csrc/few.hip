@@ -25,9 +25,9 @@
 //     are all counted;
 //   - the wave whose down item is the last on its 32 features (one from every
 //     touched expert) sums them over the k slots of every token, in slot order;
-//   - in the block's form (moe_block_forward) the items after the last down item
-//     are the rows of the residual stream: a wave waits until all of y is summed
-//     and does gate, residual sum and norms of one row.
+//   - in the block's form (moe_block_forward) the runs after the last down item
+//     are the rows of the residual stream: the workgroup that draws one waits until
+//     all of y is summed and does gate, residual sum and norms of that row.
 // Which wave does that depends on timing, what it computes does not: results
 // have the same bits on every run.
 //
@@ -575,6 +575,7 @@ struct FewPlan {
     uint32_t finished[kFewPlaces];           // gate/up items whose h is in the place
     uint32_t freed[kFewPlaces];              // the place's runs that are over
     uint32_t ready[kFewSlots];               // experts whose h is known to be there
+    float red[2][kFewWaves];                 // sums of squares of the tail
     uint32_t summed;                         // all of y is known to be there
     uint32_t polling;                        // a wave is asking memory
     unsigned long long run[kFewPlaces];      // (c + 1) << 32 | number of run c
@@ -772,76 +773,81 @@ __device__ __forceinline__ void combine_block(const FewArgs& a, const FewPlan& s
     }
 }
 
-// The block's tail on row t of y, by one wave: gate, residual sum and norms as in
-// block_norm.hip.  H <= kFewTailMaxH.
-__device__ __forceinline__ void tail_row(const FewArgs& a, int t) {
-    constexpr int V = kFewTailMaxH / 512;   // pieces of 8 channels per lane
-    const int lane = threadIdx.x & 63;
+// sum over the workgroup, in wave order
+__device__ __forceinline__ float group_sum(float v, float* red) {
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kFewWaves; ++q) s += red[q];
+    return s;
+}
+
+// The block's tail on row t of y, by the workgroup: gate, residual sum and norms
+// as in block_norm.hip.  What does not depend on y is loaded before the wait.
+template <typename Wait>
+__device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[kFewWaves], Wait wait) {
+    constexpr int NT = 64 * kFewWaves, V = kFewTailMaxH / (8 * NT);   // pieces of 8 channels per thread
     const TailArgs& T = a.tail;
     const size_t row = (size_t)t * a.H;
-    float v[V][8];
+    float v[V][8], r[V][8], wp[V][8], gt[V][8], wn[V][8];
+    int c[V];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        const int c = (64 * u + lane) * 8;
+        c[u] = (u * NT + threadIdx.x) * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-        if (c < a.H) {
-            const uint4 p0 = get16((const float*)a.y + row + c), p1 = get16((const float*)a.y + row + c + 4);
+        for (int i = 0; i < 8; ++i) { v[u][i] = 0.0f; wp[u][i] = gt[u][i] = wn[u][i] = 1.0f; }
+        if (c[u] < a.H) {
+            load8<false>(T.r, T.res_bf16, row + c[u], r[u]);
+            if (T.post_norm && T.w_post) load8<false>(T.w_post, T.param_bf16, c[u], wp[u]);
+            if (T.gate) load8<false>(T.gate, T.param_bf16, (T.gate_per_token ? row : 0) + c[u], gt[u]);
+            if (T.n_next && T.w_next) load8<false>(T.w_next, T.param_bf16, c[u], wn[u]);
+        }
+    }
+    wait();
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        if (c[u] < a.H) {
+            const uint4 p0 = get16((const float*)a.y + row + c[u]), p1 = get16((const float*)a.y + row + c[u] + 4);
             const uint32_t b[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[u][i] = __uint_as_float(b[i]);
         }
     }
-    auto rstd = [&]() {
+    auto rstd = [&](float* part) {
         float s = 0.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = fmaf(v[u][i], v[u][i], s);
-        return inv_rms(wave_sum(s), a.H, T.eps);
+            for (int i = 0; i < 8; ++i) s = fmaf(v[u][i], v[u][i], s);   // channels past H hold zeros
+        return inv_rms(group_sum(s, part), a.H, T.eps);
     };
-    auto times = [&](const void* w, size_t o, float (&x)[8]) {
-        float f[8];
-        load8<false>(w, T.param_bf16, o, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= f[i];
-    };
-    const float post = T.post_norm ? rstd() : 1.0f;
+    const float post = T.post_norm ? rstd(red[0]) : 1.0f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        const int c = (64 * u + lane) * 8;
-        if (c < a.H) {
-            if (T.post_norm) {
+        if (c[u] < a.H) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] *= post;
-                if (T.w_post) times(T.w_post, c, v[u]);
-            }
-            if (T.gate) times(T.gate, (T.gate_per_token ? row : 0) + c, v[u]);
-            float r[8];
-            load8<false>(T.r, T.res_bf16, row + c, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = fmaf(T.scale, v[u][i], r[i]);
+            for (int i = 0; i < 8; ++i) v[u][i] = fmaf(T.scale, v[u][i] * post * wp[u][i] * gt[u][i], r[u][i]);
             if (T.res_bf16) {
                 const v4u o = pack8(v[u]);
-                *(v4u*)((uint16_t*)T.r_out + row + c) = o;
+                *(v4u*)((uint16_t*)T.r_out + row + c[u]) = o;
                 unpack8(o, v[u]);   // n' is the norm of r' as stored
             } else {
-                v4f* o = (v4f*)((float*)T.r_out + row + c);
+                v4f* o = (v4f*)((float*)T.r_out + row + c[u]);
                 o[0] = v4f{v[u][0], v[u][1], v[u][2], v[u][3]};
                 o[1] = v4f{v[u][4], v[u][5], v[u][6], v[u][7]};
             }
         }
     }
     if (!T.n_next) return;
-    const float next = rstd();
+    const float next = rstd(red[1]);
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        const int c = (64 * u + lane) * 8;
-        if (c < a.H) {
+        if (c[u] < a.H) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] *= next;
-            if (T.w_next) times(T.w_next, c, v[u]);
-            *(v4u*)((uint16_t*)T.n_next + row + c) = pack8(v[u]);
+            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * next * wn[u][i];
+            *(v4u*)((uint16_t*)T.n_next + row + c[u]) = pack8(v[u]);
         }
     }
 }
@@ -942,7 +948,8 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         }
     };
     // a wave's next item, the rest of the last down run left out: every wave then
-    // ends with one item >= n3, and a workgroup's 8 waves with one whole run of them
+    // ends with one item >= n3, and a workgroup's 8 waves (8 items to a run, all
+    // earlier runs used up) with the 8 items of one run
     auto draw_down = [&]() {
         int i;
         do i = draw(ticket, s, place) - n1;
@@ -969,11 +976,11 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         if (item < n2) begin(item, it);
     }
     if (stored >= 0) finish(stored);
-    // The block's tail: behind the down items there is one for each row.
-    if (a.fuse_tail && item < n3 + a.T) {
-        wait_for(a, s, done, (uint32_t)f2, &s.summed);
-        tail_row(a, item - n3);
-    }
+    // The block's tail: the runs behind the down items are the rows, and the last
+    // run of a workgroup, one item per wave, is the same for all its waves.
+    const int t = (item - n3) / kFewWaves;
+    if (a.fuse_tail && t < a.T)
+        tail_row(a, t, s.red, [&] { wait_for(a, s, done, (uint32_t)f2, &s.summed); });
 }
 
 template <int FMT, bool PK>
@@ -998,7 +1005,7 @@ hipError_t launch_route(const FewArgs& a, hipStream_t stream) {
 hipError_t launch_few_layer(const FewArgs& a, int packed, int fp8_block, hipStream_t stream) {
     if (a.T < 1 || a.T > kFewMaxT || a.T * (a.H + 16) > kFewRowBytes || a.n_counters < few_counters(a.H))
         return hipErrorInvalidValue;
-    if (a.fuse_tail && a.H > kFewTailMaxH) return hipErrorInvalidValue;
+    if (a.fuse_tail && a.H > kFewTailMaxH) return hipErrorInvalidValue;   // the tail's registers
     const hipError_t st = fp8_block ? launch_route<true>(a, stream) : launch_route<false>(a, stream);
     if (st != hipSuccess) return st;
     if (fp8_block) return packed ? launch_layer<1, true>(a, stream) : launch_layer<1, false>(a, stream);
