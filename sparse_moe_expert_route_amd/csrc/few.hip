@@ -632,7 +632,7 @@ __device__ __forceinline__ int draw(uint32_t* ticket, FewPlan& s, int& place) {
     return uniform((int)(run * kFewWaves + pos));
 }
 
-template <int EJ>
+template <int EJ, bool SIG>
 __device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s, uint8_t* x_rows, uint32_t pitch) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     static_assert(64 * kFewWaves == 512, "one thread per expert");
@@ -642,8 +642,11 @@ __device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s, uint8_t* x
     if (tid < kFewSlots) s.ready[tid] = 0;
     if (tid == 0) { s.drawn = 0; s.summed = 0; s.polling = 0; }
     __syncthreads();
-    // the first run, while the others wait for the logits
-    if (tid == 64 * kFewWaves - 1) s.run[0] = (1ull << 32) | next_run(a.counters);
+    // the first run, drawn beside the top-k
+    uint32_t first = 0;
+    auto mid = [&] {
+        if (tid == 64 * kFewWaves - 1) first = next_run(a.counters);
+    };
     auto token = [&](int t, int id, float w) {
         if (lane < a.k) {
             s.ids[t * a.k + lane] = (int16_t)id;
@@ -655,15 +658,17 @@ __device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s, uint8_t* x
         const float* const L[2] = {a.logits + (size_t)wave * a.E, a.logits + (size_t)(wave + kFewWaves) * a.E};
         int id[2];
         float w[2];
-        topk_rows<EJ, 2, kFewParts>(L, a.bias, a.E, a.k, a.sigmoid, id, w, (size_t)a.T * a.E);
+        topk_rows<EJ, 2, kFewParts, SIG>(L, (size_t)a.T * a.E, a.bias, a.E, a.k, id, w, mid);
         token(wave, id[0], w[0]);
         token(wave + kFewWaves, id[1], w[1]);
     } else if (wave < a.T) {
         const float* const L[1] = {a.logits + (size_t)wave * a.E};
         int id[1];
         float w[1];
-        topk_rows<EJ, 1, kFewParts>(L, a.bias, a.E, a.k, a.sigmoid, id, w, (size_t)a.T * a.E);
+        topk_rows<EJ, 1, kFewParts, SIG>(L, (size_t)a.T * a.E, a.bias, a.E, a.k, id, w, mid);
         token(wave, id[0], w[0]);
+    } else {
+        mid();
     }
     // the rows of x, behind the top-k of the waves that have tokens
     const int pieces = a.H / 16;
@@ -672,6 +677,7 @@ __device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s, uint8_t* x
         const int t = i / pieces, c = i - t * pieces;
         *(uint4*)(x_rows + t * pitch + 16 * c) = *(const uint4*)(a.xq + (size_t)t * a.H + 16 * c);
     }
+    if (tid == 64 * kFewWaves - 1) s.run[0] = (1ull << 32) | first;
     __syncthreads();
     const uint32_t m = s.mask[tid];
     const unsigned long long any = __ballot(m != 0);
@@ -852,14 +858,14 @@ __device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[k
     }
 }
 
-template <int FMT, bool PK, int EJ>
+template <int FMT, bool PK, int EJ, bool SIG>
 __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a) {
     __shared__ FewPlan s;
     // FP8 rows of x, 16 bytes of padding each: the 16 rows of an MFMA operand then
     // lie on different banks
     __shared__ __attribute__((aligned(16))) uint8_t x_rows[kFewRowBytes];
     const uint32_t pitch = a.H + 16;
-    const int U = few_plan<EJ>(a, s, x_rows, pitch);
+    const int U = few_plan<EJ, SIG>(a, s, x_rows, pitch);
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int KBI = a.I / kFp8Block;
     uint32_t* ticket = a.counters;
@@ -983,12 +989,18 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         tail_row(a, t, s.red, [&] { wait_for(a, s, done, (uint32_t)f2, &s.summed); });
 }
 
-template <int FMT, bool PK>
+template <int FMT, bool PK, bool SIG>
 hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
     const dim3 grid(kFewGrid), block(64 * kFewWaves);
-    if (a.E <= 256) hipLaunchKernelGGL((few_layer_kernel<FMT, PK, 4>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((few_layer_kernel<FMT, PK, 8>), grid, block, 0, stream, a);
+    // keys per lane of the top-k: 256 and 384 experts, and the rest
+    if (a.E <= 256) hipLaunchKernelGGL((few_layer_kernel<FMT, PK, 4, SIG>), grid, block, 0, stream, a);
+    else if (a.E <= 384) hipLaunchKernelGGL((few_layer_kernel<FMT, PK, 6, SIG>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((few_layer_kernel<FMT, PK, 8, SIG>), grid, block, 0, stream, a);
     return hipGetLastError();
+}
+template <int FMT, bool PK>
+hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
+    return a.sigmoid ? launch_layer<FMT, PK, true>(a, stream) : launch_layer<FMT, PK, false>(a, stream);
 }
 
 template <bool F32S>

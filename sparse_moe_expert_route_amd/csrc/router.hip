@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(256) topk_kernel(const float* __restrict__ log
     const float* const L[1] = {logits + (size_t)t * E};
     int id[1];
     float wt[1];
-    topk_rows<EJ, 1>(L, bias, E, k, SIG, id, wt);
+    topk_rows<EJ, 1, 1, SIG>(L, 0, bias, E, k, id, wt, [] {});
     if (lane < k) {
         ids[(size_t)t * k + lane] = id[0];
         w[(size_t)t * k + lane] = wt[0];

@@ -2,9 +2,10 @@
 // router's top-k kernel and the layer for few tokens.
 //
 // key = fp32(L + b), mapped to an unsigned integer that orders like the float
-// (after -0 -> +0).  k rounds: the wave's largest key by DPP, then, of the lanes
-// and registers that hold it, the first in expert order (a ballot per register),
-// so that equal keys go to the lowest expert id; the winner retires its key.
+// (after -0 -> +0).  k rounds: each lane's largest key (equal ones: the lowest of
+// its experts), the wave's largest of those by DPP, and the lane that holds it; a
+// second maximum, over ~id, only where several lanes do, so that equal keys go to
+// the lowest expert id.  The winner retires its key.
 // Weights: softmax over the k selected *unbiased* logits, max-subtracted.
 // Several tokens share the rounds, whose dependent steps then overlap.
 #pragma once
@@ -59,15 +60,17 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// sig: sigmoid scoring (teardown "How Big Is Each Expert?": sigmoid expert
+// SIG: sigmoid scoring (teardown "How Big Is Each Expert?": sigmoid expert
 // scores and a per-expert load-balancing bias): key = fp32(sigmoid(L) + b),
 // weights = sigmoid of the selected logits over their sum.  Otherwise softmax
 // scoring as above.
 // L[n]: token n's E logits, E <= 64 EJ, each the sum of PARTS values `stride`
 // apart.  Lane j < k returns the j-th selected expert and its weight.
-template <int EJ, int N, int PARTS = 1>
-__device__ __forceinline__ void topk_rows(const float* const (&L)[N], const float* __restrict__ bias, int E, int k,
-                                          bool sig, int (&id)[N], float (&w)[N], size_t stride = 0) {
+// mid() runs once the logits have arrived (a memory access issued there is not
+// waited for by the loads' own waits).
+template <int EJ, int N, int PARTS, bool SIG, typename Mid>
+__device__ __forceinline__ void topk_rows(const float* const (&L)[N], size_t stride, const float* __restrict__ bias, int E,
+                                          int k, int (&id)[N], float (&w)[N], Mid mid) {
     const int lane = threadIdx.x & 63;
     float lv[N][EJ];
     uint32_t key[N][EJ];
@@ -95,39 +98,46 @@ __device__ __forceinline__ void topk_rows(const float* const (&L)[N], const floa
             // rounded once to float32, so that two implementations of it agree
             // on the float32 score (and with it on the selection) unless the
             // float64 value lies within an ulp or two of a float32 midpoint
-            if (sig) l = (float)(1.0 / (1.0 + exp(-(double)l)));
+            if constexpr (SIG) l = (float)(1.0 / (1.0 + exp(-(double)l)));
             lv[n][j] = l;
             // 0 is a retired key or no expert
             key[n][j] = e < E ? max(ordered_key(bias ? l + bv[j] : l), 1u) : 0u;
         }
     }
 
+    mid();
+
     float sel[N];   // lane j (< k) keeps the j-th selected logit
 #pragma unroll
     for (int n = 0; n < N; ++n) { sel[n] = 0.0f; id[n] = 0; }
     for (int r = 0; r < k; ++r) {
-        uint32_t best[N];
+        uint32_t best[N], top[N];
+        int at[N];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             best[n] = key[n][0];
+            at[n] = 0;
 #pragma unroll
-            for (int j = 1; j < EJ; ++j) best[n] = max(best[n], key[n][j]);
+            for (int j = 1; j < EJ; ++j) {
+                const bool more = key[n][j] > best[n];
+                best[n] = more ? key[n][j] : best[n];
+                at[n] = more ? j : at[n];
+            }
         }
 #pragma unroll
-        for (int n = 0; n < N; ++n) best[n] = wave_max_u32(best[n]);
+        for (int n = 0; n < N; ++n) top[n] = wave_max_u32(best[n]);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            int e = -1;
-            float l = 0.0f;
+            const unsigned long long holds = __ballot(best[n] == top[n]);
+            int owner = __builtin_ctzll(holds);
+            if (holds & (holds - 1))
+                owner = (int)(~wave_max_u32(best[n] == top[n] ? ~(uint32_t)(64 * at[n] + lane) : 0u) & 63u);
+            const int j0 = __builtin_amdgcn_readlane(at[n], owner);
+            float l = lv[n][0];
 #pragma unroll
-            for (int j = EJ - 1; j >= 0; --j) {
-                const unsigned long long holds = __ballot(key[n][j] == best[n]);
-                if (holds) {
-                    const int owner = __builtin_ctzll(holds);
-                    e = 64 * j + owner;
-                    l = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lv[n][j]), owner));
-                }
-            }
+            for (int j = 1; j < EJ; ++j) l = j == j0 ? lv[n][j] : l;
+            l = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(l), owner));
+            const int e = 64 * j0 + owner;
 #pragma unroll
             for (int j = 0; j < EJ; ++j) key[n][j] = e == lane + 64 * j ? 0u : key[n][j];
             if (lane == r) { sel[n] = l; id[n] = e; }
@@ -139,7 +149,7 @@ __device__ __forceinline__ void topk_rows(const float* const (&L)[N], const floa
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         float z;
-        if (sig) {
+        if constexpr (SIG) {
             z = lane < k ? sel[n] : 0.0f;
         } else {
             const float m = wave_max_f32(lane < k ? sel[n] : -__builtin_inff());
