@@ -18,9 +18,9 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["abi.cpp", "router.hip", "permute.hip", "prepack.hip", "expert_gemm.hip", "expert_gemm_tiled.hip",
            "expert_gemm_fp8.hip", "expert_gemm_fp8_tiled.hip", "combine.hip", "noalloc.hip", "abi_block.cpp",
-           "block_norm.hip", "few.hip"]
+           "block_norm.hip", "few.hip", "few_mxfp4.hip", "few_fp8.hip"]
 HEADERS = ["moe_launch.h", "moe_internal.h", "fp8_rows.h", "abi_checks.h", "block_launch.h", "topk_rows.h",
-           "block_rows.h"]
+           "block_rows.h", "few_layer.h"]
 # the microbenchmarks of the HBM and MFMA ceilings (include/moe_micro.h), a library of their own
 MICRO_SOURCES = ["micro.hip"]
 MICRO_LIB = os.path.join(HERE, "libmoe_micro.so")

@@ -77,5 +77,8 @@ struct FewArgs {
     float* y_slot;              // [T k][H]
 };
 hipError_t launch_few_layer(const FewArgs& a, int packed, int fp8_block, hipStream_t stream);
+// its second kernel, by the experts' format
+hipError_t launch_few_layer_mxfp4(const FewArgs& a, int packed, hipStream_t stream);
+hipError_t launch_few_layer_fp8(const FewArgs& a, int packed, hipStream_t stream);
 
 }  // namespace moe

@@ -38,8 +38,7 @@ struct NormArgs {
 
 template <int NT>
 __device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    v = wave_sum(v);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
     float s = 0.0f;

@@ -38,6 +38,12 @@ __device__ __forceinline__ v4u pack8(const float (&v)[8]) {
     return o;
 }
 
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+    return v;
+}
+
 // 1 / sqrt(sum / H + eps): a correctly rounded quotient of a correctly rounded
 // root (the hardware's reciprocal root is an ulp less exact; once per row, the
 // division costs nothing that shows)
