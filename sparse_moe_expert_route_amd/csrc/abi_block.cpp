@@ -78,7 +78,7 @@ TailArgs tail_args(const moe_block_tail& t) {
 struct BlockLayout {
     size_t layer, n, y, total;
     // few_supported() only
-    size_t counters, logits, xq, xs, hq, hs, y_slot;
+    size_t counters, logits, xq, xs, hq, hs, y_slot, part;
 };
 
 static_assert(kFewTailMaxH == MOE_BLOCK_MAX_HIDDEN && kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH &&
@@ -102,6 +102,7 @@ BlockLayout block_layout(const moe_problem& p) {
         L.hq = take(N * I);
         L.hs = take(N * (I / kFp8Block) * 4);
         L.y_slot = take(N * H * 4);
+        L.part = take(kFewPartFloats * 4);
     }
     L.total = off;
     return L;
@@ -140,6 +141,7 @@ moe_status run_few(const moe_problem& p, const void* x, const void* w_pre, const
     a.xq = at<uint8_t>(ws, L.xq); a.xs = at<void>(ws, L.xs);
     a.hq = at<uint8_t>(ws, L.hq); a.hs = at<void>(ws, L.hs);
     a.y_slot = at<float>(ws, L.y_slot);
+    a.part = at<float>(ws, L.part);
     MOE_LAUNCH(launch_few_layer(a, w.layout == MOE_WEIGHTS_PACKED, p.expert_format == MOE_EXPERTS_FP8_BLOCK, stream));
     return MOE_OK;
 }

@@ -45,10 +45,16 @@ constexpr uint32_t kErrStalled = 8u;      // error word 0: a wait inside the ker
 
 // Counters of one call: the ticket, then per touched expert (at most 8 kFewMaxT)
 // the quantised 128-channel blocks of h, then the finished down items of each
-// 32 output features, then the summed features; behind them kFewPad words that stay zero (what the kernel
+// 32 output features, then the summed features, then the finished parts of each
+// block of h; behind them kFewPad words that stay zero (what the kernel
 // loads past the end of K).
 constexpr int kFewPad = 512;
-inline int few_counters(int H) { return kFewCounterStride * (2 + 8 * kFewMaxT + H / 32) + kFewPad; }
+constexpr int kFewGrid = 256;             // workgroups of the layer kernel: one per CU
+constexpr int kFewMaxSplit = 8;           // parts of K in the gate/up items
+constexpr int kFewSplitBlocks = kFewGrid / 2;   // blocks of h at most, where K is split
+// floats of the parts' sums: 8 items of two 16 x 16 tiles to each of kFewGrid runs
+constexpr size_t kFewPartFloats = (size_t)kFewGrid * 8 * 512;
+inline int few_counters(int H) { return kFewCounterStride * (2 + 8 * kFewMaxT + H / 32 + kFewSplitBlocks) + kFewPad; }
 
 struct FewArgs {
     const uint16_t* x;          // [T][H] bf16 (null: the norm of r)
@@ -75,6 +81,7 @@ struct FewArgs {
     uint8_t* hq;                // [T k][I] e4m3
     void* hs;                   // [T k][I / 128]
     float* y_slot;              // [T k][H]
+    float* part;                // kFewPartFloats
 };
 hipError_t launch_few_layer(const FewArgs& a, int packed, int fp8_block, hipStream_t stream);
 // its second kernel, by the experts' format

@@ -20,7 +20,10 @@
 // from others is counted:
 //   - the 8 gate/up items of a workgroup's run are one 128-channel block of h,
 //     kept in LDS; the wave that completes it quantises it and counts it for its
-//     expert;
+//     expert.  With few blocks, K is cut into S parts, a run each, whose sums go
+//     through memory; the workgroup that completes the last part adds them up.
+//     (A run's 8 waves then wait for each other; they are the workgroup's 8 waves,
+//     each with one item of the run.)
 //   - a down item loads its first weights, then waits until its expert's blocks
 //     are all counted;
 //   - the wave whose down item is the last on its 32 features (one from every
@@ -58,7 +61,6 @@ namespace {
 
 constexpr int kFewWaves = 8;                  // waves per workgroup of the layer kernel
 constexpr int kFewPlaces = 4;                 // runs a workgroup can have in work
-constexpr int kFewGrid = 256;                 // its workgroups: one per CU
 constexpr int kFewSlots = kFewMaxT * 8;       // routing slots, and so touched experts, at most
 constexpr uint32_t kFewMaxPolls = 1u << 23;
 
@@ -165,21 +167,22 @@ struct FewPtrs {
     uint32_t wo, wso;        // the lane's place in a tile and in its scales
     uint32_t xo, xso;        // its token row and that row's scales
     int KB;                  // 128-column blocks of K
-    int nst, first;          // stages of K, and the one the item starts with (it wraps around)
+    int all;                 // stages of K
+    int lo, nst, first;      // the item's stages [lo, lo + nst), from lo + first on, wrapping around
     const uint8_t* pad;      // zeros
 
-    // The item's i-th stage; nst for every i past its end.  Loads past the end go
+    // The item's i-th stage; `all` for every i past its end.  Loads past the end go
     // to the pad (one cached line or a few) and add nothing: with them every load
     // is unconditional, and each wait on the in-order load counter covers the
     // stage about to be used and no later one.
     __device__ __forceinline__ int stage(int i) const {
         const int q = i + first;
-        return i >= nst ? nst : q >= nst ? q - nst : q;
+        return i >= nst ? all : lo + (q >= nst ? q - nst : q);
     }
     template <bool PAD>
-    __device__ __forceinline__ const uint8_t* base(const uint8_t* p, int st) const { return !PAD || st < nst ? p : pad; }
+    __device__ __forceinline__ const uint8_t* base(const uint8_t* p, int st) const { return !PAD || st < all ? p : pad; }
     template <bool PAD>
-    __device__ __forceinline__ uint32_t off(uint32_t o, int st) const { return !PAD || st < nst ? o : 0u; }
+    __device__ __forceinline__ uint32_t off(uint32_t o, int st) const { return !PAD || st < all ? o : 0u; }
 };
 
 template <int FMT, bool PK>
@@ -187,7 +190,8 @@ __device__ __forceinline__ void few_lane_offsets(FewPtrs& P, int K) {
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     constexpr int per = FewStageW<FMT>::kCols / kFp8Block;
     P.KB = K / kFp8Block;
-    P.nst = (P.KB + per - 1) / per;
+    P.all = P.nst = (P.KB + per - 1) / per;
+    P.lo = 0;
     if constexpr (FMT == 0) {
         P.wo = 16 * r;
         P.wso = 4 * r;
@@ -510,6 +514,8 @@ struct FewPlan {
     uint32_t drawn;                          // items handed to waves
     uint32_t read[kFewPlaces];               // waves that have their item of the place's runs
     uint32_t finished[kFewPlaces];           // gate/up items whose h is in the place
+    uint32_t summed_parts[kFewPlaces];       // gate/up items whose part is in memory
+    uint32_t verdict[kFewPlaces];            // 2 x runs counted for their block, + 1 if the last was its last part
     uint32_t freed[kFewPlaces];              // the place's runs that are over
     uint32_t ready[kFewSlots];               // experts whose h is known to be there
     float red[2][kFewWaves];                 // sums of squares of the tail
@@ -521,6 +527,9 @@ struct FewPlan {
 
 template <typename T>
 __device__ __forceinline__ T lds_load(T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP); }
+__device__ __forceinline__ void lds_store(uint32_t* p, uint32_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
 __device__ __forceinline__ uint32_t lds_add(uint32_t* p) {
     return __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
@@ -575,7 +584,7 @@ __device__ __forceinline__ int few_plan(const FewArgs& a, FewPlan& s, uint8_t* x
     static_assert(64 * kFewWaves == 512, "one thread per expert");
     static_assert(kFewMaxT <= 2 * kFewWaves, "two tokens per wave");
     s.mask[tid] = 0;
-    if (tid < kFewPlaces) { s.read[tid] = 0; s.finished[tid] = 0; s.freed[tid] = 0; s.run[tid] = 0; }
+    if (tid < kFewPlaces) { s.read[tid] = 0; s.finished[tid] = 0; s.summed_parts[tid] = 0; s.verdict[tid] = 0; s.freed[tid] = 0; s.run[tid] = 0; }
     if (tid < kFewSlots) s.ready[tid] = 0;
     if (tid == 0) { s.drawn = 0; s.summed = 0; s.polling = 0; }
     __syncthreads();
@@ -804,6 +813,19 @@ __device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[k
     }
 }
 
+// Parts into which K of the gate/up items is cut: with fewer blocks of h than
+// half the workgroups, the rest would only wait (a workgroup streams about 25 GB/s
+// per microsecond-long latency of its own: 8 experts of a four-way split Pro layer,
+// 32 blocks, took 38 us on 32 CUs).  At least two stages to a part.  By the sizes
+// alone, not by the touched experts, so that the order of a token's sums does not
+// depend on the other tokens' routing.
+__device__ __forceinline__ int split_of(const FewArgs& a, int stage_cols) {
+    const int blocks = min(a.T * a.k, a.E) * (a.I / kFp8Block), stages = (a.H + stage_cols - 1) / stage_cols;
+    int S = 1;
+    while (2 * S * blocks <= kFewGrid && 4 * S <= stages && S < kFewMaxSplit) S *= 2;
+    return S;
+}
+
 template <int FMT, bool PK, int EJ, bool SIG, bool XB>
 __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a) {
     __shared__ FewPlan s;
@@ -819,8 +841,11 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     uint32_t* fb_count = ready + kFewSlots * kFewCounterStride;           // [H / 32] down items
     const int f2 = a.H / 32;
     uint32_t* done = fb_count + f2 * kFewCounterStride;                   // summed features of y, in 32s
-    const uint8_t* pad = (const uint8_t*)(done + kFewCounterStride);      // kFewPad words of zeros
-    const int f1 = a.I / 16, n1 = U * f1;                                 // gate/up items (runs: 128-channel blocks)
+    uint32_t* parts = done + kFewCounterStride;                           // finished parts of a block of h
+    const uint8_t* pad = (const uint8_t*)(parts + kFewSplitBlocks * kFewCounterStride);   // kFewPad words of zeros
+    // gate/up items: 8 to a run, which is a 128-channel block of h or one of its S parts
+    const int S = split_of(a, FewStageW<FMT>::kCols);
+    const int n1 = U * KBI * S * kFewWaves;
     const int n2 = U * f2;                                                // down items
     const int n3 = (n2 + kFewWaves - 1) / kFewWaves * kFewWaves;          // first item behind their runs
     const uint32_t xs_row = (a.H / kFp8Block) * (FMT == 1 ? 4 : 1), hs_row = KBI * (FMT == 1 ? 4 : 1);
@@ -828,29 +853,80 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     int place;
     int item = draw(ticket, s, place);
     while (item < n1) {
-        const int u = item / f1, f = item - u * f1;
+        const int run = item / kFewWaves, bg = run / S, ks = run - bg * S;
+        const int u = bg / KBI, blk = bg - u * KBI, f = item % kFewWaves;   // 16 features of the block
         const int e = uniform(s.expert[u]), n = __popc(uniform(s.mask[e]));
         const uint32_t slot = s.slot[u][min(r, n - 1)];
+        const int row0 = blk * kFp8Block + 16 * f;
         FewPtrs P;
         P.pad = pad;
         few_lane_offsets<FMT, PK>(P, a.H);
-        few_tile<FMT>(P, 0, a.w13, a.w13_scale, (size_t)e * 2 * a.I + 16 * f, a.H);
-        few_tile<FMT>(P, 1, a.w13, a.w13_scale, (size_t)e * 2 * a.I + a.I + 16 * f, a.H);
+        few_tile<FMT>(P, 0, a.w13, a.w13_scale, (size_t)e * 2 * a.I + row0, a.H);
+        few_tile<FMT>(P, 1, a.w13, a.w13_scale, (size_t)e * 2 * a.I + a.I + row0, a.H);
         const uint32_t t = slot / (uint32_t)a.k;
         P.xs = (const uint8_t*)a.xs;
         P.xso = t * xs_row;
+        P.lo = ks * P.all / S;
+        P.nst = (ks + 1) * P.all / S - P.lo;
         // the run's 8 items start at 8 different places of K (see expert_gemm.hip):
         // their rows lie 8 K or 16 K bytes apart and read in step would fall on
         // the same memory channels
-        P.first = f % kFewWaves * P.nst / kFewWaves;
+        P.first = f * P.nst / kFewWaves;
         v4f acc[2];
         few_item<FMT, PK, XB>(P, x_rows + t * pitch, acc);
-        if (r < n) {
-            // silu(gate) * up of features 16 f + 4 g ..
+        bool whole = true;
+        if (S > 1) {
+            // The part's sums go to memory.  The wave that finishes the run counts it
+            // for its block; where it was the block's last part, every wave adds up the
+            // parts of its own 16 features, in their order.
+            auto part = [&](int q) { return a.part + (((size_t)(bg * S + q) * kFewWaves + f) * 64 + lane) * 8; };
+            if (r < n) {
+                put16(part(ks), acc[0]);
+                put16(part(ks) + 4, acc[1]);
+            }
+            wave_done();
+            uint32_t before = 0;
+            if (lane == 0) before = lds_add(&s.summed_parts[place]);
+            before = (uint32_t)uniform((int)before);
+            const uint32_t runs = before / kFewWaves + 1;   // of this place, this one included
+            if (before % kFewWaves == kFewWaves - 1) {
+                whole = count(parts + bg * kFewCounterStride) == (uint32_t)(S - 1);
+                if (lane == 0) lds_store(&s.verdict[place], 2 * runs + (whole ? 1u : 0u));
+            } else {
+                uint32_t v = 0;
+                while (((v = (uint32_t)uniform((int)lds_load(&s.verdict[place]))) >> 1) != runs) __builtin_amdgcn_s_sleep(1);
+                asm volatile("" ::: "memory");
+                whole = v & 1u;
+            }
+            if (whole && r < n) {
+                v4f sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                uint4 p[kFewMaxSplit][2];
+#pragma unroll
+                for (int q = 0; q < kFewMaxSplit; ++q) {
+                    if (q < S) {
+                        p[q][0] = get16(part(q));
+                        p[q][1] = get16(part(q) + 4);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kFewMaxSplit; ++q) {
+                    if (q < S) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            sum[i] += v4f{__uint_as_float(p[q][i].x), __uint_as_float(p[q][i].y), __uint_as_float(p[q][i].z),
+                                          __uint_as_float(p[q][i].w)};
+                    }
+                }
+                acc[0] = sum[0];
+                acc[1] = sum[1];
+            }
+        }
+        if (whole && r < n) {
+            // silu(gate) * up of features 16 f + 4 g .. of the block
             v4f h;
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[i] = silu_f32(acc[0][i]) * acc[1][i];
-            *(v4f*)&s.h[place][r][16 * (f % 8) + 4 * g] = h;
+            *(v4f*)&s.h[place][r][16 * f + 4 * g] = h;
         }
         // LDS serves a wave's accesses in order: the h of 8 counted items is there
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
@@ -858,9 +934,11 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         if (lane == 0) before = lds_add(&s.finished[place]);
         if (uniform((int)before) % kFewWaves == kFewWaves - 1) {
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-            quantise_h_block<FMT == 1>(a, s, place, u, n, f / 8);
-            wave_done();
-            count(ready + u * kFewCounterStride);
+            if (whole) {
+                quantise_h_block<FMT == 1>(a, s, place, u, n, blk);
+                wave_done();
+                count(ready + u * kFewCounterStride);
+            }
             if (lane == 0) lds_add(&s.freed[place]);
         }
         item = draw(ticket, s, place);

@@ -102,20 +102,31 @@ def test_forward_few_parity(moe, case, fmt, packed):
     assert np.array_equal(host(yb.contiguous()), bf16_rne(host(y)))
 
 
-def test_rows_do_not_depend_on_their_neighbours(moe):
-    """A token's output has the same bits alone and among others (every step is row-local)."""
-    lay = make(dict(T=16, E=32, k=4, H=1024, I=512))
+@pytest.mark.parametrize("T,over", [(16, dict(E=32, k=4, H=1024, I=512)), (3, dict(E=64, k=2, H=2048, I=256)),
+                                    (2, dict(E=16, k=2, H=4096, I=128, format="fp8_block"))])
+def test_rows_do_not_depend_on_their_neighbours(moe, T, over):
+    """A token's output has the same bits whatever the other tokens of a batch of the same size are, and
+    the same values up to float32 sums in another order alone (the gate/up sums may be cut differently)."""
+    lay = make(dict(T=T, **over))
     p = problem(lay)
+    H = p.hidden
     W = weights(lay, True)
     x, wr = dev(lay["x"]), dev(lay["w_router"])
-    y = torch.empty(16, 1024, device="cuda")
-    moe.forward_few(p, x, wr, None, W, y, moe.alloc_block_workspace(p))
-    for t in (0, 7, 15):
-        p1 = moe.Problem.make(1, 1024, 512, 32, 4)
-        y1 = torch.empty(1, 1024, device="cuda")
+    ws = moe.alloc_block_workspace(p)
+    y = torch.empty(T, H, device="cuda")
+    moe.forward_few(p, x, wr, None, W, y, ws)
+    for t in (0, T - 1):
+        others = x.roll(3, dims=1) * 0.5
+        others[t] = x[t]
+        y2 = torch.empty(T, H, device="cuda")
+        moe.forward_few(p, others.contiguous(), wr, None, W, y2, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y2[t], y[t]), t
+        p1 = moe.Problem.make(1, H, p.intermediate, p.num_experts, p.top_k, 0, p.expert_format)
+        y1 = torch.empty(1, H, device="cuda")
         moe.forward_few(p1, x[t:t + 1], wr, None, W, y1, moe.alloc_block_workspace(p1))
         torch.cuda.synchronize()
-        assert torch.equal(y1[0], y[t]), t
+        assert float((y1[0] - y[t]).norm()) <= 2e-3 * float(y[t].norm()), t
 
 
 def test_selection_ties_go_to_the_lowest_id(moe):
