@@ -448,7 +448,7 @@ __device__ __forceinline__ void few_item(const FewPtrs& P, const uint8_t* row, v
                 }
             };
             __builtin_amdgcn_sched_barrier(0);
-            compute_bf16<FMT>(P, st, w[i], rows, xs[i], acc);
+            if (at + i < nst) compute_bf16<FMT>(P, st, w[i], rows, xs[i], acc);
             __builtin_amdgcn_sched_barrier(0);
             load(at + i + R, i);
         }
