@@ -17,12 +17,13 @@ import torch
 
 import sparse_moe_expert_route_amd as _moe
 
-__all__ = ["BlockTail", "FEW_MAX_TOKENS", "BLOCK_MAX_HIDDEN", "block_workspace_size", "alloc_block_workspace",
+__all__ = ["BlockTail", "FEW_MAX_TOKENS", "BLOCK_MAX_HIDDEN", "DEVERR_STALLED", "block_workspace_size", "alloc_block_workspace",
            "block_norm", "block_residual", "combine_residual", "forward_few", "block_forward",
            "EXPORTED_BLOCK_SYMBOLS"]
 
 FEW_MAX_TOKENS = 16        # MOE_FEW_MAX_TOKENS of moe_block.h
 BLOCK_MAX_HIDDEN = 16384   # MOE_BLOCK_MAX_HIDDEN
+DEVERR_STALLED = 8         # MOE_DEVERR_STALLED
 
 EXPORTED_BLOCK_SYMBOLS = ["moe_block_workspace_size", "moe_block_norm", "moe_block_residual", "moe_combine_residual",
                           "moe_forward_few", "moe_block_forward"]
@@ -38,6 +39,13 @@ class _Tail(ctypes.Structure):
 
 
 _lib = None
+_fns = {}
+
+# the current stream's handle and the current device, without building their Python objects (a call on
+# a decode batch is bound by what happens on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _load():
@@ -57,6 +65,7 @@ def _load():
     L.moe_block_forward.argtypes = [P, vp, vp, vp, W, B, vp, sz, vp]
     for name in EXPORTED_BLOCK_SYMBOLS[1:]:
         getattr(L, name).restype = ctypes.c_int
+        _fns[name] = getattr(L, name)
     _lib = L
     return L
 
@@ -70,7 +79,7 @@ def _code(t, name):
 
 
 def _check(t, shape, name, device, dtype=None):
-    if t.dtype != dtype and dtype is not None:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
@@ -94,11 +103,16 @@ def _p(t):
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current; raises MoeError on a status."""
-    if stream is not None and stream.device_index != device:
+    if _lib is None:
+        _load()
+    f = _fns[fn]
+    if stream is None:
+        s = _raw_stream(device)
+    elif stream.device_index == device:
+        s = stream.cuda_stream
+    else:
         raise ValueError("stream must be a stream of the tensors' device")
-    f = getattr(_load(), fn)
-    s = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if torch.cuda.current_device() == device:
+    if _current_device() == device:
         st = f(*args, s)
     else:
         with torch.cuda.device(device):

@@ -789,7 +789,7 @@ __device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[k
     for (int u = 0; u < V; ++u) {
         if (c[u] < a.H) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = fmaf(T.scale, v[u][i] * post * wp[u][i] * gt[u][i], r[u][i]);
+            for (int i = 0; i < 8; ++i) v[u][i] = fmaf(T.scale, v[u][i] * (post * wp[u][i]) * gt[u][i], r[u][i]);
             if (T.res_bf16) {
                 const v4u o = pack8(v[u]);
                 *(v4u*)((uint16_t*)T.r_out + row + c[u]) = o;
@@ -807,7 +807,7 @@ __device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[k
     for (int u = 0; u < V; ++u) {
         if (c[u] < a.H) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * next * wn[u][i];
+            for (int i = 0; i < 8; ++i) v[u][i] *= next * wn[u][i];
             *(v4u*)((uint16_t*)T.n_next + row + c[u]) = pack8(v[u]);
         }
     }

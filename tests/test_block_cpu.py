@@ -48,6 +48,7 @@ def test_header_declares_the_binding_symbols(lib):
         assert hasattr(lib, n), n
     assert "MOE_FEW_MAX_TOKENS %d" % moe.FEW_MAX_TOKENS in text
     assert "MOE_BLOCK_MAX_HIDDEN %d" % moe.BLOCK_MAX_HIDDEN in text
+    assert "MOE_DEVERR_STALLED %d" % moe.DEVERR_STALLED in text
 
 
 @pytest.mark.parametrize("T,H,I,E,k,fmt", [(1, 4096, 2048, 256, 8, 0), (16, 6144, 2048, 384, 8, 1), (0, 256, 128, 8, 2, 0),
@@ -87,7 +88,7 @@ def test_tail_refusals(lib, call):
             return lib.moe_block_residual(p, 2 * M, 1, t, None)
         if call == "combine":
             return lib.moe_combine_residual(p, 2 * M, 3 * M, 4 * M, t, None)
-        return lib.moe_block_forward(p, 5 * M, 6 * M, None, _w(), t, 64 * M, 1 << 22, None)
+        return lib.moe_block_forward(p, 5 * M, 6 * M, None, _w(), t, 64 * M, BIG, None)
     for name in ("r", "r_out"):
         assert run(**{name: None}) == INVALID, name
     for name in ("r", "r_out", "w_post", "gate", "w_next", "n_next"):
@@ -126,7 +127,10 @@ def test_few_refusals(lib):
     def few(p=None, x=M, wr=2 * M, b=None, w=None, y=3 * M, od=0, ws=64 * M, n=BIG):
         return lib.moe_forward_few(_P() if p is None else p, x, wr, b, _w() if w is None else w, y, od, ws, n, None)
     assert few(p=_P(T=17)) == UNSUPPORTED
-    assert few(p=_P(H=65536 + 128)) == UNSUPPORTED and few(p=_P(I=65536 + 128)) == UNSUPPORTED
+    assert few(p=_P(T=1, H=65536 + 128)) == UNSUPPORTED and few(p=_P(I=65536 + 128)) == UNSUPPORTED
+    # the rows of x have to fit LDS: num_tokens * (hidden + 16) <= 122880
+    assert few(p=_P(T=16, H=7680)) == UNSUPPORTED and few(p=_P(T=15, H=8192)) == UNSUPPORTED
+    assert few(p=_P(T=16, H=7552), n=16) == SMALL and few(p=_P(T=14, H=8192), n=16) == SMALL
     assert few(p=_P(H=200)) == INVALID and few(p=_P(sf=3)) == UNSUPPORTED
     assert few(x=None) == INVALID and few(wr=None) == INVALID and few(y=None) == INVALID
     assert few(x=M + 8) == INVALID and few(b=M + 4) == INVALID and few(y=M + 8) == INVALID

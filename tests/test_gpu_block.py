@@ -1,9 +1,10 @@
 """GPU parity of the norms around the layer, the gate and the residual sum against the float64 oracle.
 
 Tolerances, counted in roundings (u = 2^-24, half an ulp of float32; b = 2^-8, half a step of bf16):
-  * a float32 norm: the sum of squares is a chain of at most 64 fused additions per lane, 6 across
-    the wave and 4 across the waves (74 u, halved by the root), the quotient by H, the sum with eps,
-    the root, its reciprocal and two products (6 u): NORM_U = 43 u of the value;
+  * a float32 norm: the sum of squares is a chain of at most 64 fused additions (a lane's, its wave's
+    and the waves'), 10 more leave room for another split of the row (74 u, halved by the root), the
+    quotient by H, the sum with eps, the root, its reciprocal and two products (6 u): NORM_U = 43 u of
+    the value;
   * r': the norm's error times scale * gate, 3 more products, and one rounding of the sum;
   * bf16 outputs: b of the value on top; n' is compared with the norm of the stored r'.
 """
