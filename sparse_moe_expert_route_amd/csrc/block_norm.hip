@@ -41,8 +41,12 @@ struct NormArgs {
     const void* w_pre;           // kFromR
     uint16_t* n;                 // kFromR
     TailArgs t;
+    int64_t T;
     int H;
 };
+
+// a launch has fewer than 2^32 threads along x
+constexpr int64_t kMaxGrid = 1 << 20;
 
 template <int NT>
 __device__ __forceinline__ float block_sum(float v, float* red) {
@@ -58,7 +62,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <int SRC, int NT, int V>
 __global__ void __launch_bounds__(NT) block_norm_kernel(NormArgs a) {
     __shared__ float red[2][NT / 64];
-    const size_t row = (size_t)blockIdx.x * a.H;
     const void* wn = SRC == kFromR ? a.w_pre : a.t.w_post;
     const bool norm = SRC == kFromR || a.t.post_norm;
     int c[V];
@@ -68,10 +71,15 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(NormArgs a) {
         c[u] = (u * NT + threadIdx.x) * 8;
         in[u] = c[u] < a.H;
     }
+    // rows past kMaxGrid run on along y (a loop over rows instead: norm 100 -> 118 us,
+    // combine 232 -> 289 us)
+    const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (t >= a.T) return;
+    const size_t row = (size_t)t * a.H;
     // ---- the row: r, y, or the weighted sum of its slots' rows ----
     float v[V][8];
     if constexpr (SRC == kFromRows) {
-        const size_t s0 = (size_t)blockIdx.x * a.k;
+        const size_t s0 = (size_t)t * a.k;
         int rows[8];
         float ws[8];
 #pragma unroll
@@ -169,8 +177,9 @@ __global__ void __launch_bounds__(NT) block_norm_kernel(NormArgs a) {
 }
 
 template <int SRC>
-hipError_t launch_rows(const NormArgs& a, int64_t T, hipStream_t stream) {
-    const dim3 grid((unsigned)T);
+hipError_t launch_rows(NormArgs a, int64_t T, hipStream_t stream) {
+    a.T = T;
+    const dim3 grid((unsigned)(T < kMaxGrid ? T : kMaxGrid), (unsigned)((T + kMaxGrid - 1) / kMaxGrid));
     // as many threads as the row has pieces of 8 channels: the residual of 8191 x
     // 4096 takes 75 us with 512 threads and 78 with 256 (two pieces each)
     if (a.H <= 2048) hipLaunchKernelGGL((block_norm_kernel<SRC, 256, 1>), grid, dim3(256), 0, stream, a);

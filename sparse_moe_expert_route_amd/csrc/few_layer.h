@@ -101,9 +101,11 @@ __device__ __forceinline__ uint32_t count(uint32_t* c) {
 // codes as stored, at a fifth of the vector instructions, but its internal sum
 // keeps about 13 bits below its largest product, which moves h enough to flip
 // some of its FP8 codes (error of y against 64 bits, 16 tokens of the Flash
-// layer with MXFP4 experts: 4e-4, with the bf16 MFMA 2e-7).  The conversions stay
-// under the memory time.  Down, whose result is not rounded to FP8 again, runs on
-// the block-scaled MFMA.
+// layer with MXFP4 experts: 4e-4, with the bf16 MFMA 2e-5).  The conversions stay
+// under the memory time (16 tokens of the Pro layer: 350 us either way; one token
+// of the Flash layer: 39.6 us against 38.9).  Down, whose result is not rounded to FP8 again, runs on
+// the block-scaled MFMA (on the bf16 MFMA the error would be 2e-7, at 369 us and
+// 43.6 us).
 //
 // A dot product may take K in any order as long as both operands do: on the bf16
 // MFMA a lane's 32 columns go to 4 instructions, 8 at a time.
@@ -287,7 +289,6 @@ __device__ __forceinline__ void load_row_scales(const FewPtrs& P, int st, FewSca
 // rows that other workgroups of this launch wrote, with their scales
 template <int FMT>
 __device__ __forceinline__ void load_rows(const FewPtrs& P, int st, FewStageX<FMT>& s) {
-    
 #pragma unroll
     for (int i = 0; i < (FMT == 1 ? 2 : 4); ++i)
 #pragma unroll
@@ -814,9 +815,9 @@ __device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[k
 }
 
 // Parts into which K of the gate/up items is cut: with fewer blocks of h than
-// half the workgroups, the rest would only wait (a workgroup streams about 25 GB/s
-// per microsecond-long latency of its own: 8 experts of a four-way split Pro layer,
-// 32 blocks, took 38 us on 32 CUs).  At least two stages to a part.  By the sizes
+// half the workgroups, the rest would only wait (four-way split Pro layer: 32
+// blocks for one token, 31 us in parts and 38 us whole; one token of the Flash
+// layer, 128 blocks, 38.8 and 39.6 us).  At least two stages to a part.  By the sizes
 // alone, not by the touched experts, so that the order of a token's sums does not
 // depend on the other tokens' routing.
 __device__ __forceinline__ int split_of(const FewArgs& a, int stage_cols) {
@@ -1017,7 +1018,8 @@ template <int FMT, bool PK, int EJ, bool SIG>
 hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
     const dim3 grid(kFewGrid), block(64 * kFewWaves);
     // x as bf16 in LDS where it fits (16 tokens up to H = 3832, 14 at 4096, 9 at
-    // 6144): a third fewer conversions
+    // 6144): a third fewer conversions (one token of the Flash layer 39.6 us, 40.7
+    // without; 3 of the canonical four-way split Pro layer 64.7 and 67.5)
     if (a.T * (2 * a.H + 16) <= kFewRowBytes)
         hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, true>), grid, block, 0, stream, a);
     else

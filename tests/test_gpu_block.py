@@ -225,6 +225,29 @@ def test_other_streams_and_graphs(moe):
         assert all(torch.equal(a, b) for a, b in zip(want, (n, tail.r_out, tail.n_next)))
 
 
+def test_more_rows_than_workgroups(moe):
+    """Past 2^20 rows a workgroup takes several: the rows around the border and the last ones."""
+    T, H = (1 << 20) + 77, 128
+    p = moe.Problem.make(T, H, 128, 8, 1)
+    r = torch.randn(T, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    tail = moe.BlockTail(r, torch.empty_like(r), w_next=torch.ones(H, device="cuda"), n_next=torch.empty_like(r))
+    n = torch.empty_like(r)
+    moe.block_norm(p, r, None, n)
+    moe.block_residual(p, r, tail)
+    torch.cuda.synchronize()
+    pick = torch.tensor([0, 1, 76, 77, 78, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, T - 1], device="cuda")
+    q = moe.Problem.make(len(pick), H, 128, 8, 1)
+    rp = r[pick].contiguous()
+    few = moe.BlockTail(rp, torch.empty_like(rp), w_next=tail.w_next, n_next=torch.empty_like(rp))
+    np_ = torch.empty_like(rp)
+    moe.block_norm(q, rp, None, np_)
+    moe.block_residual(q, rp, few)
+    torch.cuda.synchronize()
+    assert torch.equal(n[pick], np_) and torch.equal(tail.r_out[pick], few.r_out) and torch.equal(tail.n_next[pick], few.n_next)
+    # every row was written: the norm of any row has a root mean square of 1
+    assert float((n.float().square().mean(1) - 1).abs().max()) < 0.05
+
+
 def test_repeated_calls_give_the_same_bits(moe):
     T, H = 128, 6144
     g = torch.Generator().manual_seed(6)

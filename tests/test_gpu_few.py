@@ -129,6 +129,67 @@ def test_rows_do_not_depend_on_their_neighbours(moe, T, over):
         assert float((y1[0] - y[t]).norm()) <= 2e-3 * float(y[t].norm()), t
 
 
+def test_every_slot_its_own_expert(moe):
+    """16 tokens x 8 slots on 128 different experts, the most that can be touched."""
+    T, k, E, H = 16, 8, 128, 256
+    lay = make(dict(T=T, E=E, k=k, H=H, I=128))
+    x = np.zeros((T, H), np.float32)
+    w = np.zeros((E, H), np.float32)
+    rng = np.random.default_rng(4)
+    x[:, 32:] = 0.25 * rng.normal(size=(T, H - 32))
+    for t in range(T):
+        x[t, t] = 4.0
+        w[k * t:k * t + k, t] = 1.0 + np.arange(k) / 8
+    lay["x"], lay["w_router"] = bf16_rne(x), bf16_rne(w)
+    p = problem(lay)
+    y = torch.empty(T, H, device="cuda")
+    moe.forward_few(p, dev(lay["x"]), dev(lay["w_router"]), None, weights(lay, True), y, moe.alloc_block_workspace(p))
+    torch.cuda.synchronize()
+    ref = oracle_with_allowance(lay)
+    assert len(np.unique(ref["ids"])) == 128
+    check_output(host(y), ref)
+
+
+@pytest.mark.parametrize("over", [dict(T=16, E=64, k=8, H=1024, I=512), dict(T=2, E=16, k=4, H=4096, I=256),
+                                  dict(T=9, E=32, k=4, H=512, I=384, format="fp8_block")])
+def test_a_workspace_serves_other_inputs(moe, over):
+    """Calls with changing inputs on one workspace, back to back: each has the bits of a call with a
+    workspace of its own (nothing of an earlier call is read, from memory or from a cache)."""
+    lay = make(over)
+    p = problem(lay)
+    W, wr = weights(lay, True), dev(lay["w_router"])
+    T, H = lay["x"].shape
+    xs = [dev(S.bf16_normal(100 + i, 5, (T, H), 1.0)) for i in range(4)]
+    want = []
+    for x in xs:
+        y = torch.empty(T, H, device="cuda")
+        moe.forward_few(p, x, wr, None, W, y, moe.alloc_block_workspace(p))
+        want.append(y)
+    ws = moe.alloc_block_workspace(p)
+    got = [torch.empty(T, H, device="cuda") for _ in range(24)]
+    for i, y in enumerate(got):
+        moe.forward_few(p, xs[i % 4], wr, None, W, y, ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i % 4]) for i, y in enumerate(got))
+    assert moe.error_words(ws) == (0, 0)
+
+
+def test_other_batches_of_the_library_between(moe):
+    """The block's workspace also serves moe_forward, and calls of both may alternate on it."""
+    lay = make(dict(T=6, E=16, k=4, H=512, I=256))
+    p = problem(lay)
+    W, x, wr, ws = weights(lay, True), dev(lay["x"]), dev(lay["w_router"]), moe.alloc_block_workspace(p)
+    a, b = torch.empty(6, 512, device="cuda"), torch.empty(6, 512, device="cuda")
+    moe.forward_few(p, x, wr, None, W, a, ws)
+    moe.forward(p, x, wr, None, W, b, ws)
+    first = a.clone(), b.clone()
+    for _ in range(3):
+        moe.forward(p, x, wr, None, W, b, ws)
+        moe.forward_few(p, x, wr, None, W, a, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, first[0]) and torch.equal(b, first[1])
+
+
 def test_selection_ties_go_to_the_lowest_id(moe):
     """Equal router rows give equal logits: the lowest ids win, as moe_route selects."""
     E, k, T, H = 48, 6, 4, 256
@@ -196,7 +257,9 @@ def test_two_streams_and_graph_replays(moe):
 BLOCKS = [dict(T=1, E=32, k=4, H=512, I=256), dict(T=16, E=24, k=8, H=1024, I=512, score="sigmoid", bias="zipf"),
           dict(T=3, E=8, k=2, H=128, I=128, format="fp8_block"), dict(T=40, E=16, k=4, H=512, I=512),
           dict(T=300, E=8, k=4, H=512, I=512), dict(T=12, E=40, k=6, H=640, I=384, format="fp8_block"),
-          dict(T=2, E=16, k=8, H=6144, I=512), dict(T=5, E=4, k=1, H=2176, I=128)]
+          dict(T=2, E=16, k=8, H=6144, I=512), dict(T=5, E=4, k=1, H=2176, I=128),
+          # a down run that is not full (7 experts x 12 items), 16 rows of the tail behind it; long rows of the tail
+          dict(T=16, E=7, k=7, H=384, I=256), dict(T=7, E=4, k=2, H=16384, I=128), dict(T=3, E=4, k=2, H=8320, I=256)]
 
 
 @pytest.mark.parametrize("case", range(len(BLOCKS)))
