@@ -366,12 +366,13 @@ moe_status moe_combine(const moe_problem* p, const float* y_perm, const int32_t*
     return MOE_OK;
 }
 
-moe_status moe_forward(const moe_problem* p, const void* x_bf16, const void* w_router_bf16, const float* sel_bias,
-                       const moe_expert_weights* weights, void* y, int32_t out_dtype, void* ws, size_t ws_bytes,
-                       hipStream_t stream) {
-    MOE_CHECK(check_forward_args(p, x_bf16, w_router_bf16, sel_bias, weights, y, out_dtype));
-    MOE_CHECK(check_ws(*p, ws, ws_bytes));
-    if (p->num_tokens == 0) return MOE_OK;
+}  // extern "C"
+
+namespace moe {
+
+// The layer up to the rows that combine sums: y_perm, and where each token's are.
+moe_status forward_rows(const moe_problem* p, const void* x_bf16, const void* w_router_bf16, const float* sel_bias,
+                        const moe_expert_weights* weights, void* ws, ExpertRows* out, hipStream_t stream) {
     const Layout L = layout_of(*p);
     float* logits = at<float>(ws, L.logits);
     int32_t* ids = at<int32_t>(ws, L.ids);
@@ -393,8 +394,24 @@ moe_status moe_forward(const moe_problem* p, const void* x_bf16, const void* w_r
     MOE_CHECK(run_permute(*p, ids, x_bf16, offsets, st, ros, xq, xs, ws, stream, &planned, true, quantised));
     MOE_CHECK(run_gemm1(*p, kGemm1Swiglu, xq, xs, offsets, *weights, hq, hs, ws, !planned, stream, st));
     MOE_CHECK(run_gemm2(*p, hq, hs, offsets, *weights, y_perm, ws, false, stream));
-    MOE_LAUNCH(launch_combine(y_perm, ros, w, y, out_dtype == MOE_OUT_BF16, p->num_tokens, p->hidden, p->top_k,
-                              stream));
+    *out = ExpertRows{y_perm, ros, w};
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_forward(const moe_problem* p, const void* x_bf16, const void* w_router_bf16, const float* sel_bias,
+                       const moe_expert_weights* weights, void* y, int32_t out_dtype, void* ws, size_t ws_bytes,
+                       hipStream_t stream) {
+    MOE_CHECK(check_forward_args(p, x_bf16, w_router_bf16, sel_bias, weights, y, out_dtype));
+    MOE_CHECK(check_ws(*p, ws, ws_bytes));
+    if (p->num_tokens == 0) return MOE_OK;
+    ExpertRows rows;
+    MOE_CHECK(forward_rows(p, x_bf16, w_router_bf16, sel_bias, weights, ws, &rows, stream));
+    MOE_LAUNCH(launch_combine(rows.y_perm, rows.row_of_slot, rows.w, y, out_dtype == MOE_OUT_BF16, p->num_tokens,
+                              p->hidden, p->top_k, stream));
     return MOE_OK;
 }
 

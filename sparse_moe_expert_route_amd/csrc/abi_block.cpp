@@ -76,9 +76,9 @@ TailArgs tail_args(const moe_block_tail& t) {
 // The layer's own workspace first (so that its error words stay where
 // moe_error_words_offset says), then the block's intermediates.
 struct BlockLayout {
-    size_t layer, n, y, total;
+    size_t layer, n, total;
     // few_supported() only
-    size_t counters, logits, xq, xs, hq, hs, y_slot, part;
+    size_t y, counters, logits, xq, xs, hq, hs, y_slot, part;
 };
 
 static_assert(kFewTailMaxH == MOE_BLOCK_MAX_HIDDEN && kFewMaxT == MOE_FEW_MAX_TOKENS && kFewMaxWidth == MOE_FEW_MAX_WIDTH &&
@@ -92,8 +92,8 @@ BlockLayout block_layout(const moe_problem& p) {
     auto take = [&](size_t bytes) { const size_t o = off; off += round_up(bytes ? bytes : 1); return o; };
     L.layer = take(moe_workspace_size(&p));
     L.n = take(T * H * 2);
-    L.y = take(T * H * 4);
     if (few_supported(p)) {
+        L.y = take(T * H * 4);
         const size_t I = (size_t)p.intermediate, N = T * (size_t)p.top_k;
         L.counters = take((size_t)few_counters(p.hidden) * 4);
         L.logits = take(kFewParts * T * (size_t)p.num_experts * 4);
@@ -222,13 +222,15 @@ moe_status moe_block_forward(const moe_problem* p, const void* w_pre, const void
     if (p->num_tokens == 0) return MOE_OK;
     const BlockLayout L = block_layout(*p);
     uint16_t* n = at<uint16_t>(ws, L.n);
-    float* y = at<float>(ws, L.y);
     if (few_supported(*p))
-        return run_few(*p, nullptr, w_pre, tail, w_router_bf16, sel_bias, *weights, y, false, ws, stream);
+        return run_few(*p, nullptr, w_pre, tail, w_router_bf16, sel_bias, *weights, at<float>(ws, L.y), false, ws,
+                       stream);
     MOE_LAUNCH(launch_block_norm(tail->r, tail->res_dtype == MOE_OUT_BF16, w_pre, tail->param_dtype == MOE_OUT_BF16,
                                  tail->eps, n, p->num_tokens, p->hidden, stream));
-    MOE_CHECK(moe_forward(p, n, w_router_bf16, sel_bias, weights, y, MOE_OUT_F32, ws, ws_bytes, stream));
-    MOE_LAUNCH(launch_block_residual(y, 0, tail_args(*tail), p->num_tokens, p->hidden, stream));
+    ExpertRows rows;
+    MOE_CHECK(forward_rows(p, n, w_router_bf16, sel_bias, weights, ws, &rows, stream));
+    MOE_LAUNCH(launch_combine_residual(rows.y_perm, rows.row_of_slot, rows.w, tail_args(*tail), p->num_tokens, p->hidden,
+                                       p->top_k, stream));
     return MOE_OK;
 }
 

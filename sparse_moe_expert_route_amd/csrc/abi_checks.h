@@ -46,6 +46,18 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// What the expert GEMMs leave in the workspace for a combine.
+struct ExpertRows {
+    const float* y_perm;
+    const int32_t* row_of_slot;
+    const float* w;
+};
+
+// The launches of moe_forward but its combine, on checked arguments, num_tokens > 0
+// and a workspace of moe_workspace_size bytes (abi.cpp).
+moe_status forward_rows(const moe_problem* p, const void* x_bf16, const void* w_router_bf16, const float* sel_bias,
+                        const moe_expert_weights* weights, void* ws, ExpertRows* out, hipStream_t stream);
+
 inline bool all_aligned() { return true; }
 template <typename P, typename... R>
 inline bool all_aligned(P p, R... rest) { return p && aligned16(p) && all_aligned(rest...); }

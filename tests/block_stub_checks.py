@@ -65,9 +65,9 @@ def test_few_carves_its_workspace(lib, T, H, I, E, k, fmt):
 
 
 @pytest.mark.parametrize("T,H,I,expect", [(1, 4096, 2048, {"few": 1, "few_tail": 1}), (16, 6144, 2048, {"few": 1, "few_tail": 1}),
-                                          (17, 4096, 2048, {"norm": 1, "residual": 1}), (8, 16384, 128, {"norm": 1, "residual": 1}),
-                                          (2, 512, 65536 + 128, {"norm": 1, "residual": 1}),
-                                          (8192, 4096, 2048, {"norm": 1, "residual": 1})])
+                                          (17, 4096, 2048, {"norm": 1, "combine": 1}), (8, 16384, 128, {"norm": 1, "combine": 1}),
+                                          (2, 512, 65536 + 128, {"norm": 1, "combine": 1}),
+                                          (8192, 4096, 2048, {"norm": 1, "combine": 1})])
 def test_block_forward_launches(lib, T, H, I, expect):
     step = 1 << 42
     p = moe.Problem.make(T, H, I, 256, 8)

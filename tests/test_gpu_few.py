@@ -70,7 +70,10 @@ CASES = [dict(T=1), dict(T=16), dict(T=7, E=32, k=4, bias="zipf"), dict(T=1, H=1
          dict(T=16, H=640, I=1152, E=24, k=8), dict(T=4, H=2176, I=128, E=16, k=2), dict(T=9, H=256, I=2048, E=8, k=6),
          dict(T=16, E=64, k=8, H=512, I=512, same=True), dict(T=15, E=16, k=3, same=True),
          dict(T=8, H=4096, I=2048, E=16, k=8), dict(T=2, H=6144, I=512, E=16, k=8), dict(T=1, H=8192, I=256, E=8, k=4),
-         dict(T=2, H=16512, I=128, E=4, k=2)]
+         dict(T=2, H=16512, I=128, E=4, k=2),
+         # x too long for bf16 in LDS, with stages that end K early; K in 8, 4 and 2 parts
+         dict(T=16, H=4224, I=128, E=8, k=2), dict(T=3, H=6144, I=128, E=8, k=2), dict(T=2, H=4096, I=256, E=16, k=8),
+         dict(T=11, H=5120, I=384, E=24, k=2), dict(T=4, H=512, I=256, E=400, k=8)]
 
 
 @pytest.mark.parametrize("packed", [False, True])
@@ -316,6 +319,81 @@ def test_block_forward_parity(moe, case, res, post, gate, in_place):
     assert np.all(err[clear] <= tol[clear]), np.max((err - tol)[clear])
     nn = OB.rms_norm(got, f64(w_next))
     assert np.all(np.abs(f64(n_next) - nn) <= np.abs(nn) * (2.0 ** -8 + 1e-5))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8_block"])
+@pytest.mark.parametrize("T", [17, 64, 333])
+def test_a_prompts_block_is_its_parts(moe, T, fmt):
+    """Past the few tokens: the bits of norm, forward and residual one after the other."""
+    lay = make(dict(T=T, E=16, k=4, H=640, I=384, format=fmt))
+    p = problem(lay)
+    g = torch.Generator().manual_seed(T)
+    r = torch.randn(T, 640, generator=g).cuda()
+    par = lambda *s: (1 + 0.2 * torch.randn(*s, generator=g)).cuda()
+    wn, post, gate, nxt = par(640), par(640), par(T, 640), par(640)
+    W, wr, ws = weights(lay, T != 64), dev(lay["w_router"]), moe.alloc_block_workspace(p)
+    bf = lambda: torch.empty(T, 640, dtype=torch.bfloat16, device="cuda")
+    tails = [moe.BlockTail(r, torch.empty_like(r), post_norm=True, w_post=post, gate=gate, scale=0.7, w_next=nxt,
+                           n_next=bf()) for _ in range(2)]
+    n, y = bf(), torch.empty(T, 640, device="cuda")
+    moe.block_norm(p, r, wn, n)
+    moe.forward(p, n, wr, None, W, y, ws)
+    moe.block_residual(p, y, tails[0])
+    ws.fill_(0xFF)
+    moe.block_forward(p, wn, wr, None, W, tails[1], ws)
+    torch.cuda.synchronize()
+    assert torch.equal(tails[0].r_out, tails[1].r_out) and torch.equal(tails[0].n_next, tails[1].n_next)
+
+
+@pytest.mark.parametrize("T,over", [(1, dict(E=32, k=4, H=2048, I=256)), (16, dict(E=64, k=8, H=1024, I=512)),
+                                    (12, dict(E=16, k=4, H=512, I=256, format="fp8_block")),
+                                    (48, dict(E=16, k=4, H=512, I=256))])
+def test_block_graph_on_its_own_stream(moe, T, over):
+    """Two blocks in a row, captured, replayed with eager work and new inputs between the replays."""
+    lay = make(dict(T=T, **over))
+    p = problem(lay)
+    H = lay["x"].shape[1]
+    g = torch.Generator().manual_seed(T)
+    ins = [torch.randn(T, H, generator=g).cuda() for _ in range(3)]
+    r, ws = torch.empty_like(ins[0]), moe.alloc_block_workspace(p)
+    W, wr = weights(lay, True), dev(lay["w_router"])
+    nn = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(r)
+    first = moe.BlockTail(r, r)
+    second = moe.BlockTail(r, out, post_norm=True, w_next=torch.ones(H, device="cuda"), n_next=nn)
+
+    def run():
+        for tail in (first, second):
+            moe.block_forward(p, None, wr, None, W, tail, ws)
+
+    want = []
+    for x in ins:
+        r.copy_(x)
+        run()
+        torch.cuda.synchronize()
+        want.append((out.clone(), nn.clone()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        r.copy_(ins[0])
+        run()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+    torch.cuda.synchronize()
+    for i in range(9):
+        r.copy_(ins[i % 3])
+        out.zero_(), nn.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i % 3][0]) and torch.equal(nn, want[i % 3][1])
+        if i % 3 == 1:                                       # eager work on the same workspace between replays
+            r.copy_(ins[2])
+            run()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[2][0])
+    assert moe.error_words(ws) == (0, 0)
 
 
 def test_few_equals_forward_closely_on_a_decode_layer(moe):
