@@ -24,8 +24,9 @@
  * overwritten; argument errors found before anything is enqueued;
  * num_tokens == 0 returns MOE_OK and launches nothing; inputs finite, and every
  * sum of squares inside the float32 range.  hidden is at most
- * MOE_BLOCK_MAX_HIDDEN here (MOE_ERR_UNSUPPORTED above).  Calls captured into a
- * graph may be replayed; calls that can overlap need a workspace each.
+ * MOE_BLOCK_MAX_HIDDEN where a norm is taken (MOE_ERR_UNSUPPORTED above).  Calls
+ * captured into a graph may be replayed; calls that can overlap need a workspace
+ * each.
  */
 #ifndef MOE_BLOCK_MI355X_H
 #define MOE_BLOCK_MI355X_H
@@ -101,9 +102,10 @@ moe_status moe_combine_residual(const moe_problem* problem, const float* y_perm,
 
 /* The whole layer for few tokens: num_tokens <= MOE_FEW_MAX_TOKENS, hidden and
  * intermediate <= MOE_FEW_MAX_WIDTH and num_tokens * (hidden + 16) <=
- * MOE_FEW_MAX_ROW_BYTES (MOE_ERR_UNSUPPORTED above): the computation of moe_forward with every rounding of its
- * definition (FP8 activations, FP8 h), in two launches.  Float32 sums are
- * taken in another order than moe_forward's.  With FP8 block-scaled experts the
+ * MOE_FEW_MAX_ROW_BYTES (MOE_ERR_UNSUPPORTED above): the computation of
+ * moe_forward with every rounding of its definition (FP8 activations, FP8 h), in
+ * two launches.  Float32 sums are taken in another order than moe_forward's, one
+ * that depends on the sizes alone.  With FP8 block-scaled experts the
  * activation and h scales are the float32 product amax * (1 / 448), at most an
  * ulp from moe_forward's quotient (bf16 activations often lie on the border of
  * two codes, so about one code in a thousand differs); codes are the e4m3
@@ -115,7 +117,8 @@ moe_status moe_forward_few(const moe_problem* problem, const void* x_bf16, const
 
 /* The block: n = RMSNorm(tail->r; w_pre), the layer on n, the tail.  w_pre is
  * [H] tail->param_dtype or NULL (= 1).  Any num_tokens; within
- * the limits of moe_forward_few the layer runs as there.                   */
+ * the limits of moe_forward_few the layer runs as there, beyond them as in
+ * moe_forward (the bits of norm, moe_forward and residual in turn).         */
 moe_status moe_block_forward(const moe_problem* problem, const void* w_pre, const void* w_router_bf16,
                              const float* sel_bias, const moe_expert_weights* weights, const moe_block_tail* tail,
                              void* workspace, size_t workspace_bytes, hipStream_t stream);
