@@ -294,15 +294,34 @@ __device__ __forceinline__ void load_row_scales(const FewPtrs& P, int st, FewSca
         s.xs = load_xs<SHARED, uint8_t>(xs + P.off<!SHARED>(P.xso + min(4 * st + (int)((threadIdx.x & 63) >> 4), P.KB - 1), st));
     }
 }
-// rows that other workgroups of this launch wrote, with their scales
-template <int FMT>
-__device__ __forceinline__ void load_rows(const FewPtrs& P, int st, FewStageX<FMT>& s) {
+// rows that other workgroups of this launch wrote, with their scales: in memory
+struct FewRowsMemory {
+    template <int FMT>
+    __device__ __forceinline__ void load(const FewPtrs& P, int st, FewStageX<FMT>& s) const {
 #pragma unroll
-    for (int i = 0; i < (FMT == 1 ? 2 : 4); ++i)
+        for (int i = 0; i < (FMT == 1 ? 2 : 4); ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s.x[i][h] = get16(P.x + (P.xo + row_col<FMT, false>(P, st, i, h)));
-    load_row_scales<FMT, true>(P, st, s);
-}
+            for (int h = 0; h < 2; ++h) s.x[i][h] = get16(P.x + (P.xo + row_col<FMT, false>(P, st, i, h)));
+        load_row_scales<FMT, true>(P, st, s);
+    }
+};
+// ... or copied to LDS (the lane's row, its scales)
+struct FewRowsLds {
+    const uint8_t *row, *scales;
+    template <int FMT>
+    __device__ __forceinline__ void load(const FewPtrs& P, int st, FewStageX<FMT>& s) const {
+#pragma unroll
+        for (int i = 0; i < (FMT == 1 ? 2 : 4); ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) s.x[i][h] = *(const uint4*)(row + row_col<FMT, false>(P, st, i, h));
+        if constexpr (FMT == 1) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) s.xs[b] = *(const float*)(scales + 4 * min(2 * st + b, P.KB - 1));
+        } else {
+            s.xs = scales[min(4 * st + (int)((threadIdx.x & 63) >> 4), P.KB - 1)];
+        }
+    }
+};
 
 // 8 codes -> 8 bf16 times a power of two (exact)
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -479,8 +498,8 @@ __device__ __forceinline__ void down_prefetch(const FewPtrs& P, FewStageW<FMT> (
         if (i < P.nst) load_weights<FMT, PK, false>(P, P.stage(i), w[i]);
 }
 
-template <int FMT, bool PK>
-__device__ __forceinline__ void down_item(const FewPtrs& P, FewStageW<FMT> (&w)[kDownW], v4f (&acc)[2]) {
+template <int FMT, bool PK, typename Rows>
+__device__ __forceinline__ void down_item(const FewPtrs& P, const Rows& rows, FewStageW<FMT> (&w)[kDownW], v4f (&acc)[2]) {
     const int nst = P.nst;
     FewStageX<FMT> x[kDownX];
     static_assert(kDownW % kDownX == 0, "the rows' places repeat with the weights'");
@@ -489,14 +508,14 @@ __device__ __forceinline__ void down_item(const FewPtrs& P, FewStageW<FMT> (&w)[
     auto compute = [&](int at, int i) { compute_scaled<FMT>(P, P.stage(at), w[i % kDownW], x[i % kDownX], acc); };
 #pragma unroll
     for (int i = 0; i < kDownX; ++i)
-        if (i < nst) load_rows<FMT>(P, P.stage(i), x[i]);
+        if (i < nst) rows.template load<FMT>(P, P.stage(i), x[i]);
     int st = 0;
     for (; st + 2 * kDownW <= nst; st += kDownW) {
 #pragma unroll
         for (int i = 0; i < kDownW; ++i) {
             compute(st + i, i);
             __builtin_amdgcn_sched_barrier(0);
-            load_rows<FMT>(P, P.stage(st + i + kDownX), x[i % kDownX]);
+            rows.template load<FMT>(P, P.stage(st + i + kDownX), x[i % kDownX]);
             load_weights<FMT, PK, false>(P, P.stage(st + i + kDownW), w[i]);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -505,7 +524,7 @@ __device__ __forceinline__ void down_item(const FewPtrs& P, FewStageW<FMT> (&w)[
 #pragma unroll
     for (int i = 0; i < 2 * kDownW - 1; ++i) {
         if (st + i < nst) compute(st + i, i);
-        if (st + i + kDownX < nst) load_rows<FMT>(P, P.stage(st + i + kDownX), x[i % kDownX]);
+        if (st + i + kDownX < nst) rows.template load<FMT>(P, P.stage(st + i + kDownX), x[i % kDownX]);
         if (i < kDownW - 1 && st + i + kDownW < nst) load_weights<FMT, PK, false>(P, P.stage(st + i + kDownW), w[i]);
     }
 }
@@ -546,23 +565,31 @@ __device__ __forceinline__ uint32_t next_run(uint32_t* ticket) {
     return __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Waits until *c >= n; `known`, in LDS, says that a wave has seen it.  One wave of
-// the workgroup at a time asks memory (polls of one address leave it one after
-// the other, and the counts that they wait for queue behind them); the others
-// look at LDS.
-__device__ __forceinline__ void wait_for(const FewArgs& a, FewPlan& s, const uint32_t* c, uint32_t n, uint32_t* known) {
+// Waits until poll(), which asks memory, says so; `known`, in LDS, says that a wave
+// has seen it.  One wave of the workgroup at a time asks (polls of one address
+// leave memory one after the other, and the counts that they wait for queue behind
+// them); the others look at LDS.
+template <typename Poll>
+__device__ __forceinline__ void wait_until(const FewArgs& a, FewPlan& s, uint32_t* known, Poll poll) {
     for (uint32_t i = 0; !lds_load(known); ++i) {
-        uint32_t v = 0;
-        if ((threadIdx.x & 63) == 0 && __hip_atomic_exchange(&s.polling, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) == 0) {
-            v = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (v >= n || i >= kFewMaxPolls) __hip_atomic_store(known, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-            if (v < n && i >= kFewMaxPolls) __hip_atomic_store(a.err, kErrStalled, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __hip_atomic_store(&s.polling, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        uint32_t busy = 1;
+        if ((threadIdx.x & 63) == 0) busy = __hip_atomic_exchange(&s.polling, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (!uniform((int)busy)) {
+            const bool there = poll(), over = i >= kFewMaxPolls;
+            if (there || over) lds_store(known, 1u);
+            if (!there && over) __hip_atomic_store(a.err, kErrStalled, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            lds_store(&s.polling, 0u);
+            if (there) break;
         }
-        if ((uint32_t)uniform((int)v) >= n) break;
         __builtin_amdgcn_s_sleep(8);
     }
     asm volatile("" ::: "memory");
+}
+// ... until *c >= n
+__device__ __forceinline__ void wait_for(const FewArgs& a, FewPlan& s, const uint32_t* c, uint32_t n, uint32_t* known) {
+    wait_until(a, s, known, [&] {
+        return (uint32_t)uniform((int)__hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) >= n;
+    });
 }
 
 // The wave's next item, 8 run + its place in the run; `place`: the run's place in LDS.
@@ -711,14 +738,16 @@ __device__ __forceinline__ void quantise_h_block(const FewArgs& a, const FewPlan
 }
 
 // y[t][c .. c+32) = sum_j w[t][j] y_(t,j), in slot order: 8 lanes per token.
-__device__ __forceinline__ void combine_block(const FewArgs& a, const FewPlan& s, int fb) {
+// get(slot, i): channels c + i .. of the slot's row.
+template <typename Get>
+__device__ __forceinline__ void combine_block(const FewArgs& a, const FewPlan& s, int fb, Get get) {
     const int lane = threadIdx.x & 63;
     const int c = 32 * fb + 4 * (lane & 7);
     for (int t = lane >> 3; t < a.T; t += 8) {
         uint4 p[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < a.k) p[j] = get16(a.y_slot + (size_t)(t * a.k + j) * a.H + c);
+            if (j < a.k) p[j] = get(t * a.k + j, 4 * (lane & 7));
         v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -835,7 +864,9 @@ __device__ __forceinline__ int split_of(const FewArgs& a, int stage_cols) {
     return S;
 }
 
-template <int FMT, bool PK, int EJ, bool SIG, bool XB>
+// XB: x as bf16 in LDS.  JOIN (8 routing slots at most): a down run is one block of
+// 32 features of all touched experts, on rows of h copied to LDS, and is summed there.
+template <int FMT, bool PK, int EJ, bool SIG, bool XB, bool JOIN>
 __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a) {
     __shared__ FewPlan s;
     // rows of x, 16 bytes of padding each: the 16 rows of an MFMA operand then lie
@@ -855,9 +886,10 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     // gate/up items: 8 to a run, which is a 128-channel block of h or one of its S parts
     const int S = split_of(a, FewStageW<FMT>::kCols);
     const int n1 = U * KBI * S * kFewWaves;
-    const int n2 = U * f2;                                                // down items
+    const uint32_t h_pitch = a.I + 16, hs_row = KBI * (FMT == 1 ? 4 : 1);
+    const int n2 = (JOIN ? kFewWaves : U) * f2;                         // down items
     const int n3 = (n2 + kFewWaves - 1) / kFewWaves * kFewWaves;          // first item behind their runs
-    const uint32_t xs_row = (a.H / kFp8Block) * (FMT == 1 ? 4 : 1), hs_row = KBI * (FMT == 1 ? 4 : 1);
+    const uint32_t xs_row = (a.H / kFp8Block) * (FMT == 1 ? 4 : 1);
 
     int place;
     int item = draw(ticket, s, place);
@@ -946,7 +978,10 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
             if (whole) {
                 quantise_h_block<FMT == 1>(a, s, place, u, n, blk);
                 wave_done();
-                count(ready + u * kFewCounterStride);
+                if constexpr (!JOIN) count(ready + u * kFewCounterStride);
+                else if (lane < kFewWaves)
+                    __hip_atomic_fetch_add(ready + (u * kFewWaves + lane) * kFewCounterStride, 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
             }
             if (lane == 0) lds_add(&s.freed[place]);
         }
@@ -959,9 +994,9 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     FewStageW<FMT> w[kDownW];
     auto begin = [&](int i, Item& it) {
         // the run is over for its place once its 8 waves have read it
-        if (lane == 0 && lds_add(&s.read[place]) % kFewWaves == kFewWaves - 1) lds_add(&s.freed[place]);
-        it.u = i / f2;
-        it.f = i - it.u * f2;
+        if (!JOIN && lane == 0 && lds_add(&s.read[place]) % kFewWaves == kFewWaves - 1) lds_add(&s.freed[place]);
+        it.u = JOIN ? min(i % kFewWaves, U - 1) : i / f2;
+        it.f = JOIN ? i / kFewWaves : i - it.u * f2;
         const int e = uniform(s.expert[it.u]);
         it.n = __popc(uniform(s.mask[e]));
         it.slot = s.slot[it.u][min(r, it.n - 1)];
@@ -969,22 +1004,34 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         few_lane_offsets<FMT, PK>(it.P, a.I);
         few_tile<FMT>(it.P, 0, a.w2, a.w2_scale, (size_t)e * a.H + 32 * it.f, a.I);
         few_tile<FMT>(it.P, 1, a.w2, a.w2_scale, (size_t)e * a.H + 32 * it.f + 16, a.I);
-        it.P.first = it.f % kFewWaves * it.P.nst / kFewWaves;
+        if (JOIN && i % kFewWaves >= U) it.n = it.P.nst = 0;   // fewer experts than waves: nothing to do
+        it.P.first = (JOIN ? e : it.f) % kFewWaves * it.P.nst / kFewWaves;
         it.P.x = a.hq;
         it.P.xs = (const uint8_t*)a.hs;
         it.P.xo = it.slot * a.I;
         it.P.xso = it.slot * hs_row;
         down_prefetch<FMT, PK>(it.P, w);
     };
+    auto sum = [&](int f, auto get) {
+        combine_block(a, s, f, get);
+        if (a.fuse_tail) {
+            wave_done();
+            count(done);
+        }
+    };
     auto finish = [&](int f) {
         wave_done();
-        if (count(fb_count + f * kFewCounterStride) == (uint32_t)(U - 1)) {
-            combine_block(a, s, f);
-            if (a.fuse_tail) {
-                wave_done();
-                count(done);
-            }
-        }
+        if (count(fb_count + f * kFewCounterStride) == (uint32_t)(U - 1))
+            sum(f, [&](int slot, int i) { return get16(a.y_slot + (size_t)slot * a.H + 32 * f + i); });
+    };
+    // JOIN: every expert's blocks are all counted.  Each count went to 8 counters,
+    // so that the workgroups' polls are spread over them.
+    auto all_ready = [&] {
+        uint32_t v = (uint32_t)KBI;
+        if (lane < U)
+            v = __hip_atomic_load(ready + (lane * kFewWaves + blockIdx.x % kFewWaves) * kFewCounterStride, __ATOMIC_RELAXED,
+                                  __HIP_MEMORY_SCOPE_AGENT);
+        return (bool)__all(v >= (uint32_t)KBI);
     };
     // a wave's next item, the rest of the last down run left out: every wave then
     // ends with one item >= n3, and a workgroup's 8 waves (8 items to a run, all
@@ -1001,16 +1048,59 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
     Item it;
     if (item < n2) begin(item, it);
     while (item < n2) {
-        wait_for(a, s, ready + it.u * kFewCounterStride, (uint32_t)KBI, &s.ready[it.u]);
+        if constexpr (JOIN) wait_until(a, s, &s.ready[0], all_ready);
+        else wait_for(a, s, ready + it.u * kFewCounterStride, (uint32_t)KBI, &s.ready[it.u]);
         if (stored >= 0) finish(stored);
         v4f acc[2];
-        down_item<FMT, PK>(it.P, w, acc);
-        if (r < it.n) {
-            float* o = a.y_slot + (size_t)it.slot * a.H + 32 * it.f + 4 * g;
-            put16(o, acc[0]);
-            put16(o + 16, acc[1]);
+        if constexpr (JOIN) {
+            // The expert's rows of h come to LDS, in one trip, over the rows of x:
+            // with all of h there no wave multiplies x any more.  (Waves of two runs
+            // may copy the same rows: the same bytes.)
+            uint8_t* const scales = x_rows + a.T * a.k * h_pitch;
+            const int pieces = a.I / 16;
+#pragma unroll 4
+            for (int i = lane; i < it.n * pieces; i += 64) {
+                const int j = i / pieces, c = 16 * (i - j * pieces);
+                const uint32_t slot = s.slot[it.u][j];
+                *(uint4*)(x_rows + slot * h_pitch + c) = get16(a.hq + (size_t)slot * a.I + c);
+            }
+            for (int i = lane; i < it.n * KBI; i += 64) {
+                const int j = i / KBI, b = i - j * KBI;
+                const uint32_t slot = s.slot[it.u][j];
+                if constexpr (FMT == 1) {
+                    *(float*)(scales + slot * hs_row + 4 * b) = load_xs<true, float>((const uint8_t*)a.hs + slot * hs_row + 4 * b);
+                } else {
+                    scales[slot * hs_row + b] = load_xs<true, uint8_t>((const uint8_t*)a.hs + slot * hs_row + b);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+            down_item<FMT, PK>(it.P, FewRowsLds{x_rows + it.slot * h_pitch, scales + it.slot * hs_row}, w, acc);
+        } else {
+            down_item<FMT, PK>(it.P, FewRowsMemory{}, w, acc);
         }
-        stored = it.f;
+        if constexpr (JOIN) {
+            // rows by slot, 32 channels each, where the gate/up runs keep h
+            if (r < it.n) {
+                float* o = &s.h[place][it.slot][4 * g];
+                *(v4f*)o = acc[0];
+                *(v4f*)(o + 16) = acc[1];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+            uint32_t before = 0;
+            if (lane == 0) before = lds_add(&s.finished[place]);
+            if (uniform((int)before) % kFewWaves == kFewWaves - 1) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+                sum(it.f, [&](int slot, int i) { return *(const uint4*)&s.h[place][slot][i]; });
+                if (lane == 0) lds_add(&s.freed[place]);
+            }
+        } else {
+            if (r < it.n) {
+                float* o = a.y_slot + (size_t)it.slot * a.H + 32 * it.f + 4 * g;
+                put16(o, acc[0]);
+                put16(o + 16, acc[1]);
+            }
+            stored = it.f;
+        }
         item = draw_down();
         if (item < n2) begin(item, it);
     }
@@ -1028,10 +1118,14 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
     // x as bf16 in LDS where it fits (16 tokens up to H = 3832, 14 at 4096, 9 at
     // 6144): a third fewer conversions (one token of the Flash layer 39.6 us, 40.7
     // without; 3 of the canonical four-way split Pro layer 64.7 and 67.5)
-    if (a.T * (2 * a.H + 16) <= kFewRowBytes)
-        hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, true>), grid, block, 0, stream, a);
+    const bool xb = a.T * (2 * a.H + 16) <= kFewRowBytes;
+    const int slots = a.T * a.k;
+    if (xb && slots <= kFewWaves && slots * (a.I + 16 + a.I / kFp8Block * 4) <= kFewRowBytes)
+        hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, true, true>), grid, block, 0, stream, a);
+    else if (xb)
+        hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, true, false>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, false, false>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 template <int FMT, bool PK>

@@ -132,6 +132,33 @@ def test_rows_do_not_depend_on_their_neighbours(moe, T, over):
         assert float((y1[0] - y[t]).norm()) <= 2e-3 * float(y[t].norm()), t
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "fp8_block"])
+@pytest.mark.parametrize("over", [dict(T=1, k=8), dict(T=1, k=3), dict(T=1, k=1), dict(T=2, k=4), dict(T=4, k=2), dict(T=8, k=1),
+                                  dict(T=2, k=4, same=True), dict(T=8, k=1, E=2), dict(T=1, k=8, I=2176), dict(T=1, k=8, H=128),
+                                  dict(T=2, k=4, I=5120, E=8), dict(T=1, k=8, I=15360, H=256, E=8),
+                                  dict(T=8, k=1, H=7680, I=128, E=4)])
+def test_eight_slots_at_most(moe, over, fmt):
+    """Where a workgroup holds every expert's rows of some features (up to 8 routing slots): one expert to
+    eight, several tokens of one expert, K that ends inside a stage, and rows too long for it."""
+    over = dict(dict(E=16, H=1024, I=384, format=fmt), **over)
+    log("few %s" % over)
+    lay = make(over)
+    p = problem(lay)
+    T, H = lay["x"].shape
+    ref = oracle_with_allowance(lay)
+    x, wr = dev(lay["x"]), dev(lay["w_router"])
+    bias = None if lay["bias"] is None else dev(lay["bias"])
+    for packed in (True, False):
+        ws = moe.alloc_block_workspace(p)
+        ws.fill_(0xFF)
+        y, check = guarded(T, H, torch.float32)
+        moe.forward_few(p, x, wr, bias, weights(lay, packed), y, ws)
+        torch.cuda.synchronize()
+        check()
+        assert moe.error_words(ws) == (0, 0)
+        check_output(host(y), ref, rows=clear_tokens(lay, ref["logits"]))
+
+
 def test_every_slot_its_own_expert(moe):
     """16 tokens x 8 slots on 128 different experts, the most that can be touched."""
     T, k, E, H = 16, 8, 128, 256
