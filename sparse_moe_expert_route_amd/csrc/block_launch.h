@@ -44,7 +44,8 @@ constexpr int kFewCounterStride = 32;     // words between counters: each has it
 constexpr uint32_t kErrStalled = 8u;      // error word 0: a wait inside the kernel was given up
 
 // Counters of one call: the ticket, then per touched expert (at most 8 kFewMaxT)
-// the quantised 128-channel blocks of h, then the finished down items of each
+// the quantised 128-channel blocks of h (with at most 8 experts, 8 times over: the
+// workgroups' polls are spread), then the finished down items of each
 // 32 output features, then the summed features, then the finished parts of each
 // block of h; behind them kFewPad words that stay zero (what the kernel
 // loads past the end of K).

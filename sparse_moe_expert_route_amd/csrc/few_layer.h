@@ -27,7 +27,10 @@
 //   - a down item loads its first weights, then waits until its expert's blocks
 //     are all counted;
 //   - the wave whose down item is the last on its 32 features (one from every
-//     touched expert) sums them over the k slots of every token, in slot order;
+//     touched expert) sums them over the k slots of every token, in slot order.
+//     With at most 8 routing slots (one token of a top-8 layer) a run of 8 down
+//     items is the same 32 features of every touched expert: its sum needs LDS
+//     only, and the rows of h come to LDS in one trip instead of stage by stage;
 //   - in the block's form (moe_block_forward) the runs after the last down item
 //     are the rows of the residual stream: the workgroup that draws one waits until
 //     all of y is summed and does gate, residual sum and norms of that row.
@@ -52,9 +55,9 @@
 // Measured, both kernels (packed MXFP4 layer of 256 experts, H = 4096, I = 2048;
 // reads of one contiguous chunk per workgroup reach 7.0 TB/s): 8 tokens 115 us (770
 // MB, 6.7 TB/s); 16 tokens of 384 experts with H = 6144 351 us (2.21 GB, 6.3
-// TB/s); one token 38.4 us (109 MB), of which route 4.5, the top-k and the plan 5,
-// the reads of W13 and most of W2 about 17 and the last block of h, its count, the
-// down items that wait for it and the sum 10.  As separate launches: 138, 399
+// TB/s); one token 36.4 us (109 MB), of which route 4.5, the top-k and the plan 5,
+// the reads of W13 13, the last block of h with its sums and counts 7 (the reads of
+// W2 run beside it), the down items and the sum 4.  As separate launches: 138, 399
 // and 49 us.
 #pragma once
 
@@ -100,6 +103,11 @@ __device__ __forceinline__ uint32_t count(uint32_t* c) {
     asm volatile("" ::: "memory");
     return v;
 }
+// Sums that some lanes use only: the MFMAs before need every lane (the compiler
+// may take them for the lanes' own work and move them under the mask of their use,
+// where the operands of the other lanes are not computed).
+__device__ __forceinline__ void keep_whole(v4f (&acc)[2]) { asm volatile("" : "+v"(acc[0]), "+v"(acc[1])); }
+
 // ---------------------------------------------------------------------------
 // One pipeline stage of an item: two 16-row weight tiles and the token rows.
 //
@@ -854,7 +862,7 @@ __device__ __forceinline__ void tail_row(const FewArgs& a, int t, float (*red)[k
 // Parts into which K of the gate/up items is cut: with fewer blocks of h than
 // half the workgroups, the rest would only wait (four-way split Pro layer: 32
 // blocks for one token, 31 us in parts and 38 us whole; one token of the Flash
-// layer, 128 blocks, 38.8 and 39.6 us).  At least two stages to a part.  By the sizes
+// layer, 128 blocks, 38.8 and 39.6 us, before its down runs were joined).  At least two stages to a part.  By the sizes
 // alone, not by the touched experts, so that the order of a token's sums does not
 // depend on the other tokens' routing.
 __device__ __forceinline__ int split_of(const FewArgs& a, int stage_cols) {
@@ -915,6 +923,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         P.first = f * P.nst / kFewWaves;
         v4f acc[2];
         few_item<FMT, PK, XB>(P, x_rows + t * pitch, acc);
+        keep_whole(acc);
         bool whole = true;
         if (S > 1) {
             // The part's sums go to memory.  The wave that finishes the run counts it
@@ -1078,6 +1087,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 2) few_layer_kernel(FewArgs a)
         } else {
             down_item<FMT, PK>(it.P, FewRowsMemory{}, w, acc);
         }
+        keep_whole(acc);
         if constexpr (JOIN) {
             // rows by slot, 32 channels each, where the gate/up runs keep h
             if (r < it.n) {
@@ -1119,6 +1129,10 @@ hipError_t launch_layer(const FewArgs& a, hipStream_t stream) {
     // 6144): a third fewer conversions (one token of the Flash layer 39.6 us, 40.7
     // without; 3 of the canonical four-way split Pro layer 64.7 and 67.5)
     const bool xb = a.T * (2 * a.H + 16) <= kFewRowBytes;
+    // Runs of all touched experts, where their rows of h fit in LDS: one token of
+    // the Flash layer 36.4 us and 38.6 without, FP8 experts 50.0 and 54.2, the
+    // canonical layout 43.2 and 46.0.  With more experts than waves a run would have
+    // to wait for experts that others are still at.
     const int slots = a.T * a.k;
     if (xb && slots <= kFewWaves && slots * (a.I + 16 + a.I / kFp8Block * 4) <= kFewRowBytes)
         hipLaunchKernelGGL((few_layer_kernel<FMT, PK, EJ, SIG, true, true>), grid, block, 0, stream, a);
